@@ -71,7 +71,7 @@ const char* hd_status_string(int status);
 /* Library ABI version: (major << 16) | minor. Minor 1 added RoPE, the
  * final-stream readout, the LM-head cross-entropy and its gradients,
  * final-stream-only decode and the bounded-wait self-test; minor 2 added
- * hd_build_flags. */
+ * hd_build_flags; minor 3 added the 8-bit KV cache. */
 int hd_version(void);
 
 /* How this copy of the library was built (no counterpart on the pages), a bit
@@ -318,6 +318,91 @@ int hd_decode_attn_noalloc(const void* q, const void* k_cache, const void* v_cac
                            const int32_t* seqlen, void* out, float* lse, int B, int n, int Tcap,
                            int Hq, int Hkv, int D, int mode, int W_tokens, float scale,
                            void* stream);
+
+/*
+ * The 8-bit KV cache: K and V of the expanded sequence in one byte an element,
+ * with a scale for each block of tokens, stream and KV head.
+ * Source: tahou.com page, "中间流的作用验证" (each stream keeps its own KV
+ * state: what a stream stores never depends on another stream's values) and
+ * "实验效果与成本分析" (decode is bandwidth-bound at small batch). The 8-bit
+ * formats have no counterpart on the pages.
+ *
+ *   k_codes, v_codes  one byte an element, [B, Tcap*n, Hkv, D]: position order,
+ *                     as the bf16 cache of hd_decode_attn
+ *   k_scale, v_scale  fp32 [B, Hkv, NB, n], NB = ceil(Tcap / block_tokens); the
+ *                     scale of tokens j*block_tokens .. (j+1)*block_tokens - 1 of
+ *                     stream s is at [b, hk, j, s]
+ *   value = code * scale, code = value / scale rounded to nearest, ties to even
+ *   HD_Q8_E4M3   codes are 8-bit floats (4 exponent, 3 mantissa bits); the scale
+ *                is the smallest power of two with absmax <= 448 * scale
+ *   HD_Q8_INT8   codes are two's complement; the scale is absmax / 127 rounded
+ *                up to 8 significant bits
+ *   No scale is smaller than 2^-60.
+ * Supported: D in {64, 128}, 1 <= block_tokens <= 1024 (16 to 64 are usual).
+ * Codes and scales are those hd_kv_write_q8 writes; a cache need not be
+ * initialised, but a token is read only after it was written.
+ */
+typedef enum { HD_Q8_E4M3 = 0, HD_Q8_INT8 = 1 } hd_q8_format;
+
+/*
+ * hd_kv_write_q8 - quantise K and V rows into the 8-bit cache.
+ *
+ * Row r = t*n + s of sequence b becomes position (token_offset[b] + t)*n + s,
+ * for t < lengths[b].
+ *   k, v          bf16 [B, L*n, Hkv, D]: a prompt, a chunk of one, or (L = 1) the
+ *                 new token of a decode step
+ *   token_offset  int32 [B] on the device: tokens cached before the call; NULL: 0
+ *   lengths       int32 [B] on the device, 0 <= lengths[b] <= L; NULL: L. Rows
+ *                 behind it are padding: neither read nor written.
+ * A block whose first token is written starts afresh, whatever it held. A block
+ * that was begun before keeps its scale or, where the new rows need a larger
+ * one, is raised to that, and the codes of its earlier tokens are rounded
+ * again, code * old / new. Codes of other tokens stay as they are.
+ * If a written row holds a NaN or an infinity, its block's scale of that stream
+ * and head becomes NaN (and stays so until the block starts afresh): every
+ * value of it reads as NaN, and so does each attention output that sees one.
+ * A range outside the cache (token_offset[b] < 0, lengths[b] outside [0, L],
+ * token_offset[b] + lengths[b] > Tcap) leaves that sequence's cache unchanged
+ * and records HD_ERR_DEVICE_INDEX. Sequences do not share memory; the result
+ * does not depend on the order of the kernel's blocks.
+ */
+int hd_kv_write_q8(const void* k, const void* v, const int32_t* token_offset, const int32_t* lengths,
+                   void* k_codes, void* v_codes, float* k_scale, float* v_scale, int B, int L, int n,
+                   int Tcap, int Hkv, int D, int format, int block_tokens, void* stream);
+
+/*
+ * hd_kv_read_q8 - rows of the 8-bit cache as bf16 (code * scale, rounded).
+ * Arguments as hd_kv_write_q8, with k, v the outputs, bf16 [B, L*n, Hkv, D]:
+ * tokens token_offset[b] .. token_offset[b] + lengths[b] - 1. Rows behind
+ * lengths[b], and those of a sequence whose range lies outside the cache
+ * (HD_ERR_DEVICE_INDEX), are left as they were.
+ */
+int hd_kv_read_q8(const void* k_codes, const void* v_codes, const float* k_scale, const float* v_scale,
+                  const int32_t* token_offset, const int32_t* lengths, void* k, void* v, int B, int L,
+                  int n, int Tcap, int Hkv, int D, int format, int block_tokens, void* stream);
+
+/* Bytes of workspace hd_decode_attn_q8 and hd_decode_attn_final_q8 need for
+ * these sizes, whatever the mode, format and block_tokens (0 on invalid sizes). */
+size_t hd_decode_q8_workspace_bytes(int B, int n, int Tcap, int Hq, int Hkv, int D);
+size_t hd_decode_final_q8_workspace_bytes(int B, int n, int Tcap, int Hq, int Hkv, int D);
+
+/*
+ * hd_decode_attn_q8, hd_decode_attn_final_q8 - hd_decode_attn and
+ * hd_decode_attn_final against the 8-bit cache.
+ * q, seqlen, out, lse, mode, W_tokens, scale, the precondition (the new token's
+ * n rows are in the cache) and the errors are theirs; the cache is as above.
+ * Scores and softmax are fp32 and the scales are applied in fp32; the weights
+ * are rounded to fp16 before they meet the V codes. Supported: as there.
+ */
+int hd_decode_attn_q8(const void* q, const void* k_codes, const void* v_codes, const float* k_scale,
+                      const float* v_scale, const int32_t* seqlen, void* out, float* lse, int B, int n,
+                      int Tcap, int Hq, int Hkv, int D, int format, int block_tokens, int mode,
+                      int W_tokens, float scale, void* workspace, size_t workspace_bytes, void* stream);
+int hd_decode_attn_final_q8(const void* q, const void* k_codes, const void* v_codes, const float* k_scale,
+                            const float* v_scale, const int32_t* seqlen, void* out, float* lse, int B, int n,
+                            int Tcap, int Hq, int Hkv, int D, int format, int block_tokens, int mode,
+                            int W_tokens, float scale, void* workspace, size_t workspace_bytes,
+                            void* stream);
 
 /*
  * hd_selftest_wait_timeout - test the bounded-wait failure path (no fault).

@@ -16,14 +16,20 @@ data-parallel hot path of Hidden Decoding with Stream-Factorized Attention
   optionally with final-stream-only queries (KV-mirror);
 * ``hd_decode_attn_final``  the final stream's query alone (KV-mirror layers);
 * ``hd_decode_attn``  the n stream queries of a new token against the
-  interleaved per-stream KV cache.
+  interleaved per-stream KV cache;
+* ``hd_kv_write_q8`` / ``hd_kv_read_q8``  an 8-bit KV cache (e4m3 or int8, a scale
+  for each block of tokens, stream and head): quantised as it is written, read
+  back as bf16;
+* ``hd_decode_attn_q8`` / ``hd_decode_attn_final_q8``  the decode steps against it.
 
 The C names are re-exported from ``_lib`` (pointer + size arguments). The
 tensor helpers below (``expand_embed``, ``rope_``, ``attn_fwd``, ``attn_bwd``,
-``decode_attn``, ``decode_attn_final``) allocate outputs and workspace with torch and call the same C
-entry points; torch is used for device memory and streams only.
+``decode_attn``, ``decode_attn_final``, and those of the 8-bit cache) allocate outputs and workspace with
+torch and call the same C entry points; torch is used for device memory and streams only.
 """
 from __future__ import annotations
+
+from typing import Any, NamedTuple
 
 from ._lib import (  # noqa: F401
     HD_ERR_CUDA,
@@ -32,18 +38,26 @@ from ._lib import (  # noqa: F401
     HD_ERR_TIMEOUT,
     HD_ERR_UNSUPPORTED,
     HD_OK,
+    HD_Q8_E4M3,
+    HD_Q8_INT8,
     HDError,
     hd_attn_bwd,
     hd_attn_bwd_workspace_bytes,
     hd_attn_fwd,
     hd_decode_attn,
     hd_decode_attn_final,
+    hd_decode_attn_final_q8,
     hd_decode_attn_noalloc,
+    hd_decode_attn_q8,
+    hd_decode_final_q8_workspace_bytes,
     hd_decode_final_workspace_bytes,
+    hd_decode_q8_workspace_bytes,
     hd_decode_workspace_bytes,
     hd_device_status,
     hd_expand_embed,
     hd_final_readout,
+    hd_kv_read_q8,
+    hd_kv_write_q8,
     hd_lm_head_ce,
     hd_lm_head_ce_bwd,
     hd_lm_head_ce_bwd_workspace_bytes,
@@ -225,3 +239,144 @@ def lm_head_ce_bwd(x, w, labels, lse, n, grad_scale=1.0, stream=None, workspace=
     hd_lm_head_ce_bwd(x, w, labels, lse, grad_scale, dh, dw, B, L, n, d, V, workspace,
                       workspace.numel() * workspace.element_size(), stream)
     return dh, dw
+
+
+class KVCacheQ8(NamedTuple):
+    """An 8-bit KV cache: codes [B, Tcap*n, Hkv, D], float8_e4m3fn or int8 (the format), and fp32 scales
+    [B, Hkv, ceil(Tcap / block_tokens), n]. ``kv_cache_q8`` makes one; any four tensors of these
+    shapes do."""
+
+    k: Any
+    v: Any
+    k_scale: Any
+    v_scale: Any
+    n: int
+    block_tokens: int
+
+
+def kv_cache_q8(B, Tcap, n, Hkv, D, dtype, block_tokens=16, device="cuda"):
+    """An empty 8-bit cache for ``Tcap`` tokens; ``dtype`` is torch.float8_e4m3fn or torch.int8."""
+    import torch
+
+    k, v = (torch.zeros((B, Tcap * n, Hkv, D), dtype=dtype, device=device) for _ in range(2))
+    k_scale, v_scale = (torch.zeros((B, Hkv, -(-Tcap // block_tokens), n), dtype=torch.float32, device=device)
+                        for _ in range(2))
+    return KVCacheQ8(k, v, k_scale, v_scale, n, block_tokens)
+
+
+def _cache_q8(cache):
+    """(B, Tcap, Hkv, D, format) of a KVCacheQ8, its tensors checked against one another."""
+    import torch
+
+    _need_cuda(cache.k, cache.v, cache.k_scale, cache.v_scale)
+    formats = {torch.float8_e4m3fn: HD_Q8_E4M3, torch.int8: HD_Q8_INT8}
+    if cache.k.dtype not in formats or cache.v.dtype != cache.k.dtype:
+        raise ValueError("codes must be float8_e4m3fn or int8, k and v alike")
+    if cache.n < 1 or cache.block_tokens < 1 or cache.k.dim() != 4 or cache.k.shape[1] % cache.n:
+        raise ValueError("codes must be [B, Tcap*n, Hkv, D]")
+    B, S, Hkv, D = cache.k.shape
+    Tcap = S // cache.n
+    want = (B, Hkv, -(-Tcap // cache.block_tokens), cache.n)
+    if cache.v.shape != cache.k.shape or tuple(cache.k_scale.shape) != want or tuple(cache.v_scale.shape) != want:
+        raise ValueError(f"k and v must be alike and the scales {list(want)}")
+    if cache.k_scale.dtype != torch.float32 or cache.v_scale.dtype != torch.float32:
+        raise ValueError("scales must be float32")
+    return B, Tcap, Hkv, D, formats[cache.k.dtype]
+
+
+def _same_device(device, *ts):
+    for t in ts:
+        if t is not None and t.device != device:
+            raise ValueError("tensors must live on one device")
+
+
+def _index_q8(t, B, what):
+    import torch
+
+    if t is not None:
+        _need_cuda(t)
+        if t.dtype != torch.int32 or tuple(t.shape) != (B,):
+            raise ValueError(f"{what} must be int32 [B]")
+
+
+def kv_write_q8(k, v, cache, token_offset=None, lengths=None, stream=None):
+    """Quantise k, v bf16 [B, L*n, Hkv, D] into ``cache`` (a KVCacheQ8) from token ``token_offset[b]`` on
+    (int32 [B]; None: 0). ``lengths`` (int32 [B]) gives the tokens of each sequence in a padded batch."""
+    import torch
+
+    _need_cuda(k, v)
+    B, Tcap, Hkv, D, fmt = _cache_q8(cache)
+    if k.dtype != torch.bfloat16 or v.dtype != torch.bfloat16:
+        raise ValueError("k and v must be bfloat16")
+    if k.dim() != 4 or k.shape != v.shape or k.shape[0] != B or tuple(k.shape[2:]) != (Hkv, D) or k.shape[1] % cache.n:
+        raise ValueError(f"k and v must be [{B}, L*{cache.n}, {Hkv}, {D}]")
+    _index_q8(token_offset, B, "token_offset")
+    _index_q8(lengths, B, "lengths")
+    _same_device(cache.k.device, cache.v, cache.k_scale, cache.v_scale, k, v, token_offset, lengths)
+    L = k.shape[1] // cache.n
+    if L == 0:
+        return
+    with torch.cuda.device(cache.k.device):
+        hd_kv_write_q8(k, v, token_offset, lengths, cache.k, cache.v, cache.k_scale, cache.v_scale, B, L, cache.n,
+                       Tcap, Hkv, D, fmt, cache.block_tokens, stream)
+
+
+def kv_read_q8(cache, L, token_offset=None, lengths=None, out=None, stream=None):
+    """(k, v) bf16 [B, L*n, Hkv, D]: ``L`` tokens of each sequence from ``token_offset[b]`` on, or the first
+    ``lengths[b]`` of them; the rows behind those are zeros, or what the buffers ``out`` = (k, v) held."""
+    import torch
+
+    B, Tcap, Hkv, D, fmt = _cache_q8(cache)
+    _index_q8(token_offset, B, "token_offset")
+    _index_q8(lengths, B, "lengths")
+    device, shape = cache.k.device, (B, L * cache.n, Hkv, D)
+    _same_device(device, cache.v, cache.k_scale, cache.v_scale, token_offset, lengths)
+    with torch.cuda.device(device):
+        if out is None:
+            # without lengths every row is written, unless its range lies outside the cache
+            make = torch.zeros if lengths is not None or token_offset is not None or L > Tcap else torch.empty
+            out = tuple(make(shape, dtype=torch.bfloat16, device=device) for _ in range(2))
+        k, v = out
+        _need_cuda(k, v)
+        _same_device(device, k, v)
+        if any(t.dtype != torch.bfloat16 or tuple(t.shape) != shape for t in (k, v)):
+            raise ValueError(f"out must be two bfloat16 tensors {list(shape)}")
+        if L:
+            hd_kv_read_q8(cache.k, cache.v, cache.k_scale, cache.v_scale, token_offset, lengths, k, v, B, L,
+                          cache.n, Tcap, Hkv, D, fmt, cache.block_tokens, stream)
+    return k, v
+
+
+def _decode_q8(q, cache, seqlen, mode, W, scale, stream, workspace, final):
+    import torch
+
+    _need_cuda(q, seqlen)
+    B, Tcap, Hkv, D, fmt = _cache_q8(cache)
+    nq = 1 if final else cache.n
+    if q.dtype != torch.bfloat16 or q.dim() != 4 or (q.shape[0], q.shape[1], q.shape[3]) != (B, nq, D):
+        raise ValueError(f"q must be bfloat16 [{B}, {nq}, Hq, {D}]")
+    _index_q8(seqlen, B, "seqlen")
+    _same_device(cache.k.device, cache.v, cache.k_scale, cache.v_scale, q, seqlen, workspace)
+    Hq = q.shape[2]
+    if scale is None:
+        scale = D ** -0.5
+    with torch.cuda.device(q.device):
+        out = torch.empty_like(q)
+        lse = torch.empty((B, Hq, nq), dtype=torch.float32, device=q.device)
+        size = hd_decode_final_q8_workspace_bytes if final else hd_decode_q8_workspace_bytes
+        if workspace is None:
+            workspace = torch.empty(size(B, cache.n, Tcap, Hq, Hkv, D), dtype=torch.uint8, device=q.device)
+        call = hd_decode_attn_final_q8 if final else hd_decode_attn_q8
+        call(q, cache.k, cache.v, cache.k_scale, cache.v_scale, seqlen, out, lse, B, cache.n, Tcap, Hq, Hkv, D,
+             fmt, cache.block_tokens, mode, W, scale, workspace, workspace.numel() * workspace.element_size(), stream)
+    return out, lse
+
+
+def decode_attn_q8(q, cache, seqlen, mode, W=0, scale=None, stream=None, workspace=None):
+    """decode_attn against a KVCacheQ8: q bf16 [B, n, Hq, D]; seqlen int32 [B] (tokens incl. the new one)."""
+    return _decode_q8(q, cache, seqlen, mode, W, scale, stream, workspace, False)
+
+
+def decode_attn_final_q8(q, cache, seqlen, mode, W=0, scale=None, stream=None, workspace=None):
+    """decode_attn_final against a KVCacheQ8: q bf16 [B, 1, Hq, D] (stream n-1 of the new token)."""
+    return _decode_q8(q, cache, seqlen, mode, W, scale, stream, workspace, True)

@@ -22,6 +22,9 @@ HD_ERR_CUDA = 3
 HD_ERR_TIMEOUT = 4
 HD_ERR_DEVICE_INDEX = 5
 
+HD_Q8_E4M3 = 0
+HD_Q8_INT8 = 1
+
 # every symbol include/hd.h declares, with (restype, argtypes)
 _P = ctypes.c_void_p
 _I = ctypes.c_int
@@ -51,6 +54,12 @@ SIGNATURES = {
                                   _Z, _P]),
     "hd_decode_attn_noalloc": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _F,
                                     _P]),
+    "hd_kv_write_q8": (_I, [_P] * 8 + [_I] * 8 + [_P]),
+    "hd_kv_read_q8": (_I, [_P] * 8 + [_I] * 8 + [_P]),
+    "hd_decode_q8_workspace_bytes": (_Z, [_I, _I, _I, _I, _I, _I]),
+    "hd_decode_final_q8_workspace_bytes": (_Z, [_I, _I, _I, _I, _I, _I]),
+    "hd_decode_attn_q8": (_I, [_P] * 8 + [_I] * 10 + [_F, _P, _Z, _P]),
+    "hd_decode_attn_final_q8": (_I, [_P] * 8 + [_I] * 10 + [_F, _P, _Z, _P]),
     "hd_selftest_wait_timeout": (_I, [ctypes.c_longlong, _P]),
     "hd_device_status": (_I, [_P, _I]),
 }
@@ -210,6 +219,45 @@ def hd_decode_attn_noalloc(q, k_cache, v_cache, seqlen, out, lse, B, n, Tcap, Hq
                                                ptr(out), ptr(lse), B, n, Tcap, Hq, Hkv, D, mode,
                                                W_tokens, float(scale), stream_handle(stream)),
                   "hd_decode_attn_noalloc")
+
+
+def hd_kv_write_q8(k, v, token_offset, lengths, k_codes, v_codes, k_scale, v_scale, B, L, n, Tcap, Hkv, D,
+                   fmt, block_tokens, stream=None):
+    return _check(lib().hd_kv_write_q8(ptr(k), ptr(v), ptr(token_offset), ptr(lengths), ptr(k_codes),
+                                       ptr(v_codes), ptr(k_scale), ptr(v_scale), B, L, n, Tcap, Hkv, D, fmt,
+                                       block_tokens, stream_handle(stream)), "hd_kv_write_q8")
+
+
+def hd_kv_read_q8(k_codes, v_codes, k_scale, v_scale, token_offset, lengths, k, v, B, L, n, Tcap, Hkv, D, fmt,
+                  block_tokens, stream=None):
+    return _check(lib().hd_kv_read_q8(ptr(k_codes), ptr(v_codes), ptr(k_scale), ptr(v_scale),
+                                      ptr(token_offset), ptr(lengths), ptr(k), ptr(v), B, L, n, Tcap, Hkv, D,
+                                      fmt, block_tokens, stream_handle(stream)), "hd_kv_read_q8")
+
+
+def hd_decode_q8_workspace_bytes(B, n, Tcap, Hq, Hkv, D):
+    return int(lib().hd_decode_q8_workspace_bytes(B, n, Tcap, Hq, Hkv, D))
+
+
+def hd_decode_final_q8_workspace_bytes(B, n, Tcap, Hq, Hkv, D):
+    return int(lib().hd_decode_final_q8_workspace_bytes(B, n, Tcap, Hq, Hkv, D))
+
+
+def hd_decode_attn_q8(q, k_codes, v_codes, k_scale, v_scale, seqlen, out, lse, B, n, Tcap, Hq, Hkv, D, fmt,
+                      block_tokens, mode, W_tokens, scale, workspace, workspace_bytes, stream=None):
+    return _check(lib().hd_decode_attn_q8(ptr(q), ptr(k_codes), ptr(v_codes), ptr(k_scale), ptr(v_scale),
+                                          ptr(seqlen), ptr(out), ptr(lse), B, n, Tcap, Hq, Hkv, D, fmt,
+                                          block_tokens, mode, W_tokens, float(scale), ptr(workspace),
+                                          int(workspace_bytes), stream_handle(stream)), "hd_decode_attn_q8")
+
+
+def hd_decode_attn_final_q8(q, k_codes, v_codes, k_scale, v_scale, seqlen, out, lse, B, n, Tcap, Hq, Hkv, D,
+                            fmt, block_tokens, mode, W_tokens, scale, workspace, workspace_bytes, stream=None):
+    return _check(lib().hd_decode_attn_final_q8(ptr(q), ptr(k_codes), ptr(v_codes), ptr(k_scale), ptr(v_scale),
+                                                ptr(seqlen), ptr(out), ptr(lse), B, n, Tcap, Hq, Hkv, D, fmt,
+                                                block_tokens, mode, W_tokens, float(scale), ptr(workspace),
+                                                int(workspace_bytes), stream_handle(stream)),
+                  "hd_decode_attn_final_q8")
 
 
 def hd_selftest_wait_timeout(limit_cycles, stream=None):

@@ -28,6 +28,11 @@ int* status_ptr() {
 bool aligned16(const void* ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 15u) == 0; }
 
 constexpr long long kMaxPositions = 1LL << 28;  // positions and rows stay far below kWinInf
+constexpr int kMaxBlockTokens = 1024;  // one warp quantises a block of a stream and head
+
+int q8_blocks(int tokens, int block_tokens) {
+  return static_cast<int>((static_cast<long long>(tokens) + block_tokens - 1) / block_tokens);
+}
 
 int check_attn(const void* q, const void* k, const void* v, int B, int L, int n, int Hq, int Hkv,
                int D, int mode, int W, int final_only, float scale) {
@@ -209,6 +214,119 @@ int decode_call(const void* q, const void* k_cache, const void* v_cache, const i
   return from_cuda(launch_decode(p, static_cast<cudaStream_t>(stream)));
 }
 
+int check_q8(int B, int n, int Tcap, int Hkv, int D, int format, int block_tokens) {
+  if (B < 1 || n < 1 || Tcap < 1 || Hkv < 1 || D < 1) return HD_ERR_INVALID_ARG;
+  if (format != HD_Q8_E4M3 && format != HD_Q8_INT8) return HD_ERR_INVALID_ARG;
+  if (block_tokens < 1) return HD_ERR_INVALID_ARG;
+  if (static_cast<long long>(Tcap) * n > kMaxPositions) return HD_ERR_UNSUPPORTED;
+  if (D != 64 && D != 128) return HD_ERR_UNSUPPORTED;
+  if (block_tokens > kMaxBlockTokens) return HD_ERR_UNSUPPORTED;
+  return HD_OK;
+}
+
+// Shared by the write and the read of the 8-bit cache; the caller sets the row
+// pointers.
+int kv_q8_params(KvQ8Params& p, const int32_t* token_offset, const int32_t* lengths, void* k_codes,
+                 void* v_codes, float* k_scale, float* v_scale, int B, int L, int n, int Tcap, int Hkv,
+                 int D, int format, int block_tokens) {
+  if (!k_codes || !v_codes || !k_scale || !v_scale || L < 1) return HD_ERR_INVALID_ARG;
+  const int st = check_q8(B, n, Tcap, Hkv, D, format, block_tokens);
+  if (st != HD_OK) return st;
+  if (static_cast<long long>(L) * n > kMaxPositions) return HD_ERR_UNSUPPORTED;
+  if (!aligned16(k_codes) || !aligned16(v_codes) || !aligned16(k_scale) || !aligned16(v_scale))
+    return HD_ERR_INVALID_ARG;
+  p.k_codes = static_cast<uint8_t*>(k_codes);
+  p.v_codes = static_cast<uint8_t*>(v_codes);
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.token_offset = token_offset;
+  p.lengths = lengths;
+  p.status = status_ptr();
+  p.B = B;
+  p.L = L;
+  p.n = n;
+  p.Tcap = Tcap;
+  p.Hkv = Hkv;
+  p.D = D;
+  p.format = format;
+  p.bt = block_tokens;
+  p.nb = q8_blocks(Tcap, block_tokens);
+  // L tokens touch the most blocks when they begin at a block's last token
+  p.blocks = token_offset ? q8_blocks(L - 1, block_tokens) + 1 : q8_blocks(L, block_tokens);
+  p.ext_rows = static_cast<long long>(B) * L * n * Hkv * D;
+  p.ext_codes = static_cast<long long>(B) * Tcap * n * Hkv * D;
+  p.ext_scale = static_cast<long long>(B) * Hkv * p.nb * n;
+  return HD_OK;
+}
+
+int decode_q8_call(const void* q, const void* k_codes, const void* v_codes, const float* k_scale,
+                   const float* v_scale, const int32_t* seqlen, void* out, float* lse, int B, int n,
+                   int Tcap, int Hq, int Hkv, int D, int format, int block_tokens, int mode,
+                   int W_tokens, int final_only, float scale, void* workspace, size_t workspace_bytes,
+                   void* stream) {
+  if (!q || !k_codes || !v_codes || !k_scale || !v_scale || !seqlen || !out || !lse || !workspace)
+    return HD_ERR_INVALID_ARG;
+  const int st = check_q8(B, n, Tcap, Hkv, D, format, block_tokens);
+  if (st != HD_OK) return st;
+  if (Hq < 1 || Hq % Hkv != 0) return HD_ERR_INVALID_ARG;
+  if (mode < HD_INTRA || mode > HD_CROSS_WINDOW) return HD_ERR_INVALID_ARG;
+  if (mode == HD_CROSS_WINDOW && W_tokens < 1) return HD_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || !isfinite(scale)) return HD_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k_codes) || !aligned16(v_codes) || !aligned16(k_scale) ||
+      !aligned16(v_scale) || !aligned16(out) || !aligned16(workspace))
+    return HD_ERR_INVALID_ARG;
+  if (workspace_bytes < decode_workspace(B, n, Tcap, Hq, Hkv, D, final_only)) return HD_ERR_INVALID_ARG;
+  DecodeQ8Params p = {};
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.kc = static_cast<const uint8_t*>(k_codes);
+  p.vc = static_cast<const uint8_t*>(v_codes);
+  p.ks = k_scale;
+  p.vs = v_scale;
+  p.seqlen = seqlen;
+  p.o = static_cast<__nv_bfloat16*>(out);
+  p.lse = lse;
+  p.status = status_ptr();
+  p.B = B;
+  p.n = n;
+  p.Tcap = Tcap;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.D = D;
+  p.format = format;
+  p.bt = block_tokens;
+  p.nb = q8_blocks(Tcap, block_tokens);
+  p.mode = mode;
+  const long long w = static_cast<long long>(n) * W_tokens;
+  p.win = (mode == HD_CROSS_WINDOW && w < static_cast<long long>(Tcap) * n) ? static_cast<int>(w)
+                                                                           : kWinInf;
+  if (mode == HD_CROSS_WINDOW && p.win == kWinInf) p.mode = HD_CROSS_FULL;
+  p.nq = final_only ? 1 : n;
+  p.s0 = final_only ? n - 1 : 0;
+  p.kstride = 1;
+  p.kres = 0;
+  p.kpt = n;
+  if (final_only && mode == HD_INTRA && n > 1) {
+    // the final stream's own rows only; each of them is visible to its query
+    p.kstride = n;
+    p.kres = n - 1;
+    p.kpt = 1;
+    p.mode = HD_CROSS_FULL;
+  }
+  p.rows = p.nq * (Hq / Hkv);
+  decode_split_plan(B, p.rows, static_cast<long long>(Tcap) * p.kpt, Hkv, sm_count(), &p.mt,
+                    &p.splits, &p.chunk);
+  const size_t prow = static_cast<size_t>(B) * Hkv * p.mt * 16 * p.splits;
+  p.ext_q = static_cast<long long>(B) * p.nq * Hq * D;
+  p.ext_lse = static_cast<long long>(B) * Hq * p.nq;
+  p.ext_cache = static_cast<long long>(B) * Tcap * n * Hkv * D;
+  p.ext_scale = static_cast<long long>(B) * Hkv * p.nb * n;
+  p.ext_part = static_cast<long long>(prow);
+  p.part_o = static_cast<float*>(workspace);
+  p.part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + align256(prow * D * 4));
+  p.scale_log2 = scale * 1.4426950408889634074f;
+  return from_cuda(launch_decode_q8(p, static_cast<cudaStream_t>(stream)));
+}
+
 }  // namespace
 }  // namespace hd
 
@@ -228,7 +346,7 @@ const char* hd_status_string(int status) {
   }
 }
 
-int hd_version(void) { return (1 << 16) | 2; }
+int hd_version(void) { return (1 << 16) | 3; }
 
 int hd_build_flags(void) {
 #ifdef HD_CHECK_BOUNDS
@@ -432,6 +550,60 @@ int hd_decode_attn_final(const void* q, const void* k_cache, const void* v_cache
                          void* workspace, size_t workspace_bytes, void* stream) {
   return hd::decode_call(q, k_cache, v_cache, seqlen, out, lse, B, n, Tcap, Hq, Hkv, D, mode,
                          W_tokens, 1, scale, workspace, workspace_bytes, stream);
+}
+
+int hd_kv_write_q8(const void* k, const void* v, const int32_t* token_offset, const int32_t* lengths,
+                   void* k_codes, void* v_codes, float* k_scale, float* v_scale, int B, int L, int n,
+                   int Tcap, int Hkv, int D, int format, int block_tokens, void* stream) {
+  if (!k || !v) return HD_ERR_INVALID_ARG;
+  KvQ8Params p = {};
+  const int st = kv_q8_params(p, token_offset, lengths, k_codes, v_codes, k_scale, v_scale, B, L, n, Tcap,
+                              Hkv, D, format, block_tokens);
+  if (st != HD_OK) return st;
+  if (!aligned16(k) || !aligned16(v)) return HD_ERR_INVALID_ARG;
+  p.k = static_cast<const __nv_bfloat16*>(k);
+  p.v = static_cast<const __nv_bfloat16*>(v);
+  return from_cuda(launch_kv_write_q8(p, sm_count(), static_cast<cudaStream_t>(stream)));
+}
+
+int hd_kv_read_q8(const void* k_codes, const void* v_codes, const float* k_scale, const float* v_scale,
+                  const int32_t* token_offset, const int32_t* lengths, void* k, void* v, int B, int L,
+                  int n, int Tcap, int Hkv, int D, int format, int block_tokens, void* stream) {
+  if (!k || !v) return HD_ERR_INVALID_ARG;
+  KvQ8Params p = {};
+  const int st = kv_q8_params(p, token_offset, lengths, const_cast<void*>(k_codes), const_cast<void*>(v_codes),
+                              const_cast<float*>(k_scale), const_cast<float*>(v_scale), B, L, n, Tcap, Hkv, D,
+                              format, block_tokens);
+  if (st != HD_OK) return st;
+  if (!aligned16(k) || !aligned16(v)) return HD_ERR_INVALID_ARG;
+  p.k_out = static_cast<__nv_bfloat16*>(k);
+  p.v_out = static_cast<__nv_bfloat16*>(v);
+  return from_cuda(launch_kv_read_q8(p, sm_count(), static_cast<cudaStream_t>(stream)));
+}
+
+size_t hd_decode_q8_workspace_bytes(int B, int n, int Tcap, int Hq, int Hkv, int D) {
+  return hd::decode_workspace(B, n, Tcap, Hq, Hkv, D, 0);
+}
+
+size_t hd_decode_final_q8_workspace_bytes(int B, int n, int Tcap, int Hq, int Hkv, int D) {
+  return hd::decode_workspace(B, n, Tcap, Hq, Hkv, D, 1);
+}
+
+int hd_decode_attn_q8(const void* q, const void* k_codes, const void* v_codes, const float* k_scale,
+                      const float* v_scale, const int32_t* seqlen, void* out, float* lse, int B, int n,
+                      int Tcap, int Hq, int Hkv, int D, int format, int block_tokens, int mode,
+                      int W_tokens, float scale, void* workspace, size_t workspace_bytes, void* stream) {
+  return hd::decode_q8_call(q, k_codes, v_codes, k_scale, v_scale, seqlen, out, lse, B, n, Tcap, Hq, Hkv, D,
+                            format, block_tokens, mode, W_tokens, 0, scale, workspace, workspace_bytes, stream);
+}
+
+int hd_decode_attn_final_q8(const void* q, const void* k_codes, const void* v_codes, const float* k_scale,
+                            const float* v_scale, const int32_t* seqlen, void* out, float* lse, int B, int n,
+                            int Tcap, int Hq, int Hkv, int D, int format, int block_tokens, int mode,
+                            int W_tokens, float scale, void* workspace, size_t workspace_bytes,
+                            void* stream) {
+  return hd::decode_q8_call(q, k_codes, v_codes, k_scale, v_scale, seqlen, out, lse, B, n, Tcap, Hq, Hkv, D,
+                            format, block_tokens, mode, W_tokens, 1, scale, workspace, workspace_bytes, stream);
 }
 
 int hd_selftest_wait_timeout(long long limit_cycles, void* stream) {

@@ -48,6 +48,51 @@ void decode_split_plan(int B, int rows, long long keys, int Hkv, int sms, int* m
                        int* chunk);
 cudaError_t launch_decode(const DecodeParams& p, cudaStream_t stream);
 
+// The 8-bit KV cache: rows written to or read from tokens t0 .. t0+len-1 of each
+// sequence, t0 = token_offset[b] (or 0), len = lengths[b] (or L).
+constexpr int kQ8MinExp = -60;  // the smallest scale is 2^-60
+struct KvQ8Params {
+  const __nv_bfloat16* k;  // write: [B, L*n, Hkv, D]
+  const __nv_bfloat16* v;
+  __nv_bfloat16* k_out;    // read: [B, L*n, Hkv, D]
+  __nv_bfloat16* v_out;
+  uint8_t* k_codes;        // [B, Tcap*n, Hkv, D]
+  uint8_t* v_codes;
+  float* k_scale;          // [B, Hkv, nb, n]
+  float* v_scale;
+  const int32_t* token_offset;  // [B] or null
+  const int32_t* lengths;       // [B] or null
+  int* status;
+  int B, L, n, Tcap, Hkv, D, format, bt, nb;  // nb = blocks of bt tokens in Tcap
+  int blocks;              // blocks that L tokens can touch
+  // allocated elements, for the checked build's bounds checks
+  long long ext_rows, ext_codes, ext_scale;
+};
+cudaError_t launch_kv_write_q8(const KvQ8Params& p, int sms, cudaStream_t stream);
+cudaError_t launch_kv_read_q8(const KvQ8Params& p, int sms, cudaStream_t stream);
+
+// Decode attention over the 8-bit cache. Query streams and key space as in
+// DecodeParams.
+struct DecodeQ8Params {
+  const __nv_bfloat16* q;   // [B, nq, Hq, D]
+  const uint8_t* kc;        // [B, Tcap*n, Hkv, D]
+  const uint8_t* vc;
+  const float* ks;          // [B, Hkv, nb, n]
+  const float* vs;
+  const int32_t* seqlen;    // [B]
+  __nv_bfloat16* o;         // [B, nq, Hq, D]
+  float* lse;               // [B, Hq, nq]
+  float* part_o;            // [B, Hkv, mt*16, splits, D] fp32
+  float* part_ml;           // [B, Hkv, mt*16, splits, 2] fp32 (reference in log2 units, sum)
+  int* status;
+  int B, n, Tcap, Hq, Hkv, D, mode, win, nq, s0, kstride, kres, kpt;
+  int rows, mt, splits, chunk;
+  int format, bt, nb;
+  float scale_log2;
+  long long ext_q, ext_lse, ext_cache, ext_scale, ext_part;
+};
+cudaError_t launch_decode_q8(const DecodeQ8Params& p, cudaStream_t stream);
+
 struct RopeParams {
   __nv_bfloat16* q;             // [B, Sq, Hq, D] or null
   __nv_bfloat16* k;             // [B, S, Hkv, D] or null
