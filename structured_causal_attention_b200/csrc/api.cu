@@ -259,6 +259,48 @@ int kv_q8_params(KvQ8Params& p, const int32_t* token_offset, const int32_t* leng
   return HD_OK;
 }
 
+// Problems, keys and splits of a decode step over the 8-bit cache: sets nq, s0,
+// groups, spg, kpt, win, rows, mt, splits and chunk from the sizes.
+void decode_q8_problem(DecodeQ8Params& p, int mode, int W_tokens, int final_only) {
+  p.nq = final_only ? 1 : p.n;
+  p.s0 = final_only ? p.n - 1 : 0;
+  p.groups = mode == HD_INTRA ? p.nq : 1;
+  p.spg = p.nq / p.groups;
+  p.kpt = mode == HD_INTRA ? 1 : p.n;
+  long long keys = static_cast<long long>(p.Tcap) * p.kpt;
+  p.win = kWinInf;
+  if (mode == HD_CROSS_WINDOW) {
+    const long long w = static_cast<long long>(p.n) * W_tokens;
+    if (w < keys) p.win = static_cast<int>(w);
+    // the first of nq queries begins its window nq - 1 positions before the last
+    if (w + p.nq - 1 < keys) keys = w + p.nq - 1;
+  }
+  p.rows = p.spg * (p.Hq / p.Hkv);
+  p.mt = (p.rows + 15) / 16;
+  decode_q8_plan(static_cast<long long>(p.B) * p.Hkv * p.groups * p.mt, keys, sm_count(), &p.splits, &p.chunk);
+}
+
+// The most that any mode needs of one decode step over the 8-bit cache.
+size_t decode_q8_workspace(int B, int n, int Tcap, int Hq, int Hkv, int D, int final_only) {
+  if (B < 1 || n < 1 || Tcap < 1 || Hq < 1 || Hkv < 1 || D < 1 || Hq % Hkv) return 0;
+  size_t most = 0;
+  for (int mode = HD_INTRA; mode <= HD_CROSS_FULL; ++mode) {
+    DecodeQ8Params p = {};
+    p.B = B;
+    p.n = n;
+    p.Tcap = Tcap;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    decode_q8_problem(p, mode, 1, final_only);
+    const long long problems = static_cast<long long>(B) * Hkv * p.groups * p.mt;
+    const long long splits = decode_q8_most_splits(problems, static_cast<long long>(Tcap) * p.kpt, sm_count());
+    const size_t prow = static_cast<size_t>(problems) * 16 * static_cast<size_t>(splits);
+    const size_t need = align256(prow * static_cast<size_t>(D) * 4) + align256(prow * 2 * 4);
+    if (need > most) most = need;
+  }
+  return most;
+}
+
 int decode_q8_call(const void* q, const void* k_codes, const void* v_codes, const float* k_scale,
                    const float* v_scale, const int32_t* seqlen, void* out, float* lse, int B, int n,
                    int Tcap, int Hq, int Hkv, int D, int format, int block_tokens, int mode,
@@ -275,7 +317,8 @@ int decode_q8_call(const void* q, const void* k_codes, const void* v_codes, cons
   if (!aligned16(q) || !aligned16(k_codes) || !aligned16(v_codes) || !aligned16(k_scale) ||
       !aligned16(v_scale) || !aligned16(out) || !aligned16(workspace))
     return HD_ERR_INVALID_ARG;
-  if (workspace_bytes < decode_workspace(B, n, Tcap, Hq, Hkv, D, final_only)) return HD_ERR_INVALID_ARG;
+  if (static_cast<long long>(Tcap) * n * Hkv * D >= 1LL << 40) return HD_ERR_UNSUPPORTED;  // a TMA stride
+  if (workspace_bytes < decode_q8_workspace(B, n, Tcap, Hq, Hkv, D, final_only)) return HD_ERR_INVALID_ARG;
   DecodeQ8Params p = {};
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.kc = static_cast<const uint8_t*>(k_codes);
@@ -295,35 +338,16 @@ int decode_q8_call(const void* q, const void* k_codes, const void* v_codes, cons
   p.format = format;
   p.bt = block_tokens;
   p.nb = q8_blocks(Tcap, block_tokens);
-  p.mode = mode;
-  const long long w = static_cast<long long>(n) * W_tokens;
-  p.win = (mode == HD_CROSS_WINDOW && w < static_cast<long long>(Tcap) * n) ? static_cast<int>(w)
-                                                                           : kWinInf;
-  if (mode == HD_CROSS_WINDOW && p.win == kWinInf) p.mode = HD_CROSS_FULL;
-  p.nq = final_only ? 1 : n;
-  p.s0 = final_only ? n - 1 : 0;
-  p.kstride = 1;
-  p.kres = 0;
-  p.kpt = n;
-  if (final_only && mode == HD_INTRA && n > 1) {
-    // the final stream's own rows only; each of them is visible to its query
-    p.kstride = n;
-    p.kres = n - 1;
-    p.kpt = 1;
-    p.mode = HD_CROSS_FULL;
-  }
-  p.rows = p.nq * (Hq / Hkv);
-  decode_split_plan(B, p.rows, static_cast<long long>(Tcap) * p.kpt, Hkv, sm_count(), &p.mt,
-                    &p.splits, &p.chunk);
-  const size_t prow = static_cast<size_t>(B) * Hkv * p.mt * 16 * p.splits;
+  p.scale_log2 = scale * 1.4426950408889634074f;
+  decode_q8_problem(p, mode, W_tokens, final_only);
+  if (static_cast<long long>(B) * Hkv * p.groups * p.mt * p.splits > (1LL << 31) - 1) return HD_ERR_UNSUPPORTED;
+  const size_t prow = static_cast<size_t>(B) * Hkv * p.groups * p.mt * 16 * p.splits;
   p.ext_q = static_cast<long long>(B) * p.nq * Hq * D;
   p.ext_lse = static_cast<long long>(B) * Hq * p.nq;
-  p.ext_cache = static_cast<long long>(B) * Tcap * n * Hkv * D;
   p.ext_scale = static_cast<long long>(B) * Hkv * p.nb * n;
   p.ext_part = static_cast<long long>(prow);
   p.part_o = static_cast<float*>(workspace);
   p.part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + align256(prow * D * 4));
-  p.scale_log2 = scale * 1.4426950408889634074f;
   return from_cuda(launch_decode_q8(p, static_cast<cudaStream_t>(stream)));
 }
 
@@ -582,11 +606,11 @@ int hd_kv_read_q8(const void* k_codes, const void* v_codes, const float* k_scale
 }
 
 size_t hd_decode_q8_workspace_bytes(int B, int n, int Tcap, int Hq, int Hkv, int D) {
-  return hd::decode_workspace(B, n, Tcap, Hq, Hkv, D, 0);
+  return hd::decode_q8_workspace(B, n, Tcap, Hq, Hkv, D, 0);
 }
 
 size_t hd_decode_final_q8_workspace_bytes(int B, int n, int Tcap, int Hq, int Hkv, int D) {
-  return hd::decode_workspace(B, n, Tcap, Hq, Hkv, D, 1);
+  return hd::decode_q8_workspace(B, n, Tcap, Hq, Hkv, D, 1);
 }
 
 int hd_decode_attn_q8(const void* q, const void* k_codes, const void* v_codes, const float* k_scale,

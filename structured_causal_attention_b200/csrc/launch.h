@@ -71,8 +71,10 @@ struct KvQ8Params {
 cudaError_t launch_kv_write_q8(const KvQ8Params& p, int sms, cudaStream_t stream);
 cudaError_t launch_kv_read_q8(const KvQ8Params& p, int sms, cudaStream_t stream);
 
-// Decode attention over the 8-bit cache. Query streams and key space as in
-// DecodeParams.
+// Decode attention over the 8-bit cache. The nq query streams s0 .. s0+nq-1 of
+// the new token are `groups` problems a KV head of spg streams each: under INTRA
+// one stream, whose keys are its tokens (kpt = 1); otherwise all of them, over
+// the positions (kpt = n).
 struct DecodeQ8Params {
   const __nv_bfloat16* q;   // [B, nq, Hq, D]
   const uint8_t* kc;        // [B, Tcap*n, Hkv, D]
@@ -82,15 +84,20 @@ struct DecodeQ8Params {
   const int32_t* seqlen;    // [B]
   __nv_bfloat16* o;         // [B, nq, Hq, D]
   float* lse;               // [B, Hq, nq]
-  float* part_o;            // [B, Hkv, mt*16, splits, D] fp32
-  float* part_ml;           // [B, Hkv, mt*16, splits, 2] fp32 (reference in log2 units, sum)
+  float* part_o;            // [B, Hkv, groups, mt*16, splits, D] fp32
+  float* part_ml;           // [B, Hkv, groups, mt*16, splits, 2] fp32 (reference in log2 units, sum)
   int* status;
-  int B, n, Tcap, Hq, Hkv, D, mode, win, nq, s0, kstride, kres, kpt;
-  int rows, mt, splits, chunk;
+  int B, n, Tcap, Hq, Hkv, D, nq, s0, groups, spg, kpt;
+  int win;                  // keys of the window (kWinInf: none)
+  int rows, mt, splits, chunk;  // rows = spg*(Hq/Hkv); chunk keys per split
   int format, bt, nb;
   float scale_log2;
-  long long ext_q, ext_lse, ext_cache, ext_scale, ext_part;
+  long long ext_q, ext_lse, ext_scale, ext_part;
 };
+// Splits and keys of one for `problems` (sequence, KV head, group, row tile) of up
+// to `keys` keys; fewer keys are never cut into more than most_splits of more.
+long long decode_q8_most_splits(long long problems, long long keys, int sms);
+void decode_q8_plan(long long problems, long long keys, int sms, int* splits, int* chunk);
 cudaError_t launch_decode_q8(const DecodeQ8Params& p, cudaStream_t stream);
 
 struct RopeParams {
