@@ -374,8 +374,8 @@ int hd_kv_write_q8(const void* k, const void* v, const int32_t* token_offset, co
  * hd_kv_read_q8 - rows of the 8-bit cache as bf16 (code * scale, rounded).
  * Arguments as hd_kv_write_q8, with k, v the outputs, bf16 [B, L*n, Hkv, D]:
  * tokens token_offset[b] .. token_offset[b] + lengths[b] - 1. Rows behind
- * lengths[b], and those of a sequence whose range lies outside the cache
- * (HD_ERR_DEVICE_INDEX), are left as they were.
+ * lengths[b], and all of a sequence whose range lies outside the cache
+ * (HD_ERR_DEVICE_INDEX), are zeros.
  */
 int hd_kv_read_q8(const void* k_codes, const void* v_codes, const float* k_scale, const float* v_scale,
                   const int32_t* token_offset, const int32_t* lengths, void* k, void* v, int B, int L,

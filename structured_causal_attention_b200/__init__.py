@@ -268,26 +268,32 @@ def _cache_q8(cache):
     """(B, Tcap, Hkv, D, format) of a KVCacheQ8, its tensors checked against one another."""
     import torch
 
-    _need_cuda(cache.k, cache.v, cache.k_scale, cache.v_scale)
-    formats = {torch.float8_e4m3fn: HD_Q8_E4M3, torch.int8: HD_Q8_INT8}
-    if cache.k.dtype not in formats or cache.v.dtype != cache.k.dtype:
+    k, v, k_scale, v_scale, n, block_tokens = cache
+    _need_cuda(k, v, k_scale, v_scale)
+    if v.dtype != k.dtype or k.dtype not in (torch.float8_e4m3fn, torch.int8):
         raise ValueError("codes must be float8_e4m3fn or int8, k and v alike")
-    if cache.n < 1 or cache.block_tokens < 1 or cache.k.dim() != 4 or cache.k.shape[1] % cache.n:
+    if n < 1 or block_tokens < 1 or k.dim() != 4 or k.shape[1] % n:
         raise ValueError("codes must be [B, Tcap*n, Hkv, D]")
-    B, S, Hkv, D = cache.k.shape
-    Tcap = S // cache.n
-    want = (B, Hkv, -(-Tcap // cache.block_tokens), cache.n)
-    if cache.v.shape != cache.k.shape or tuple(cache.k_scale.shape) != want or tuple(cache.v_scale.shape) != want:
+    B, S, Hkv, D = k.shape
+    Tcap = S // n
+    want = (B, Hkv, -(-Tcap // block_tokens), n)
+    if v.shape != k.shape or k_scale.shape != want or v_scale.shape != want:
         raise ValueError(f"k and v must be alike and the scales {list(want)}")
-    if cache.k_scale.dtype != torch.float32 or cache.v_scale.dtype != torch.float32:
+    if k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32:
         raise ValueError("scales must be float32")
-    return B, Tcap, Hkv, D, formats[cache.k.dtype]
+    return B, Tcap, Hkv, D, HD_Q8_E4M3 if k.dtype == torch.float8_e4m3fn else HD_Q8_INT8
 
 
-def _same_device(device, *ts):
+def _on(device, *ts):
+    """The tensors' one device as the current one: a context."""
+    import contextlib
+
+    import torch
+
     for t in ts:
         if t is not None and t.device != device:
             raise ValueError("tensors must live on one device")
+    return contextlib.nullcontext() if device.index == torch.cuda.current_device() else torch.cuda.device(device)
 
 
 def _index_q8(t, B, what):
@@ -295,7 +301,7 @@ def _index_q8(t, B, what):
 
     if t is not None:
         _need_cuda(t)
-        if t.dtype != torch.int32 or tuple(t.shape) != (B,):
+        if t.dtype != torch.int32 or t.shape != (B,):
             raise ValueError(f"{what} must be int32 [B]")
 
 
@@ -308,39 +314,33 @@ def kv_write_q8(k, v, cache, token_offset=None, lengths=None, stream=None):
     B, Tcap, Hkv, D, fmt = _cache_q8(cache)
     if k.dtype != torch.bfloat16 or v.dtype != torch.bfloat16:
         raise ValueError("k and v must be bfloat16")
-    if k.dim() != 4 or k.shape != v.shape or k.shape[0] != B or tuple(k.shape[2:]) != (Hkv, D) or k.shape[1] % cache.n:
+    if k.dim() != 4 or k.shape != v.shape or k.shape[0] != B or k.shape[2:] != (Hkv, D) or k.shape[1] % cache.n:
         raise ValueError(f"k and v must be [{B}, L*{cache.n}, {Hkv}, {D}]")
     _index_q8(token_offset, B, "token_offset")
     _index_q8(lengths, B, "lengths")
-    _same_device(cache.k.device, cache.v, cache.k_scale, cache.v_scale, k, v, token_offset, lengths)
     L = k.shape[1] // cache.n
-    if L == 0:
-        return
-    with torch.cuda.device(cache.k.device):
-        hd_kv_write_q8(k, v, token_offset, lengths, cache.k, cache.v, cache.k_scale, cache.v_scale, B, L, cache.n,
-                       Tcap, Hkv, D, fmt, cache.block_tokens, stream)
+    with _on(cache.k.device, cache.v, cache.k_scale, cache.v_scale, k, v, token_offset, lengths):
+        if L:
+            hd_kv_write_q8(k, v, token_offset, lengths, cache.k, cache.v, cache.k_scale, cache.v_scale, B, L,
+                           cache.n, Tcap, Hkv, D, fmt, cache.block_tokens, stream)
 
 
 def kv_read_q8(cache, L, token_offset=None, lengths=None, out=None, stream=None):
     """(k, v) bf16 [B, L*n, Hkv, D]: ``L`` tokens of each sequence from ``token_offset[b]`` on, or the first
-    ``lengths[b]`` of them; the rows behind those are zeros, or what the buffers ``out`` = (k, v) held."""
+    ``lengths[b]`` of them and zeros behind. ``out``: two buffers to use."""
     import torch
 
     B, Tcap, Hkv, D, fmt = _cache_q8(cache)
     _index_q8(token_offset, B, "token_offset")
     _index_q8(lengths, B, "lengths")
-    device, shape = cache.k.device, (B, L * cache.n, Hkv, D)
-    _same_device(device, cache.v, cache.k_scale, cache.v_scale, token_offset, lengths)
-    with torch.cuda.device(device):
-        if out is None:
-            # without lengths every row is written, unless its range lies outside the cache
-            make = torch.zeros if lengths is not None or token_offset is not None or L > Tcap else torch.empty
-            out = tuple(make(shape, dtype=torch.bfloat16, device=device) for _ in range(2))
-        k, v = out
-        _need_cuda(k, v)
-        _same_device(device, k, v)
-        if any(t.dtype != torch.bfloat16 or tuple(t.shape) != shape for t in (k, v)):
-            raise ValueError(f"out must be two bfloat16 tensors {list(shape)}")
+    shape = (B, L * cache.n, Hkv, D)
+    if out is None:
+        out = cache.k.new_empty(shape, dtype=torch.bfloat16), cache.k.new_empty(shape, dtype=torch.bfloat16)
+    k, v = out
+    _need_cuda(k, v)
+    if k.dtype != torch.bfloat16 or v.dtype != torch.bfloat16 or k.shape != shape or v.shape != shape:
+        raise ValueError(f"out must be two bfloat16 tensors {list(shape)}")
+    with _on(cache.k.device, cache.v, cache.k_scale, cache.v_scale, token_offset, lengths, k, v):
         if L:
             hd_kv_read_q8(cache.k, cache.v, cache.k_scale, cache.v_scale, token_offset, lengths, k, v, B, L,
                           cache.n, Tcap, Hkv, D, fmt, cache.block_tokens, stream)
@@ -352,23 +352,25 @@ def _decode_q8(q, cache, seqlen, mode, W, scale, stream, workspace, final):
 
     _need_cuda(q, seqlen)
     B, Tcap, Hkv, D, fmt = _cache_q8(cache)
-    nq = 1 if final else cache.n
-    if q.dtype != torch.bfloat16 or q.dim() != 4 or (q.shape[0], q.shape[1], q.shape[3]) != (B, nq, D):
+    n = cache.n
+    nq = 1 if final else n
+    if q.dtype != torch.bfloat16 or q.dim() != 4 or q.shape[:2] != (B, nq) or q.shape[3] != D:
         raise ValueError(f"q must be bfloat16 [{B}, {nq}, Hq, {D}]")
     _index_q8(seqlen, B, "seqlen")
-    _same_device(cache.k.device, cache.v, cache.k_scale, cache.v_scale, q, seqlen, workspace)
+    if workspace is not None:
+        _need_cuda(workspace)
     Hq = q.shape[2]
     if scale is None:
         scale = D ** -0.5
-    with torch.cuda.device(q.device):
+    with _on(q.device, cache.k, cache.v, cache.k_scale, cache.v_scale, seqlen, workspace):
         out = torch.empty_like(q)
-        lse = torch.empty((B, Hq, nq), dtype=torch.float32, device=q.device)
-        size = hd_decode_final_q8_workspace_bytes if final else hd_decode_q8_workspace_bytes
+        lse = q.new_empty((B, Hq, nq), dtype=torch.float32)
         if workspace is None:
-            workspace = torch.empty(size(B, cache.n, Tcap, Hq, Hkv, D), dtype=torch.uint8, device=q.device)
+            size = hd_decode_final_q8_workspace_bytes if final else hd_decode_q8_workspace_bytes
+            workspace = q.new_empty(size(B, n, Tcap, Hq, Hkv, D), dtype=torch.uint8)
         call = hd_decode_attn_final_q8 if final else hd_decode_attn_q8
-        call(q, cache.k, cache.v, cache.k_scale, cache.v_scale, seqlen, out, lse, B, cache.n, Tcap, Hq, Hkv, D,
-             fmt, cache.block_tokens, mode, W, scale, workspace, workspace.numel() * workspace.element_size(), stream)
+        call(q, cache.k, cache.v, cache.k_scale, cache.v_scale, seqlen, out, lse, B, n, Tcap, Hq, Hkv, D, fmt,
+             cache.block_tokens, mode, W, scale, workspace, workspace.numel() * workspace.element_size(), stream)
     return out, lse
 
 

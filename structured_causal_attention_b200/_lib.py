@@ -119,7 +119,8 @@ def stream_handle(stream) -> int:
     if stream is None:
         import torch
 
-        return int(torch.cuda.current_stream().cuda_stream)
+        # torch.cuda.current_stream().cuda_stream without making a Stream object (3 us of host time)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return int(stream.cuda_stream)

@@ -253,6 +253,13 @@ int kv_q8_params(KvQ8Params& p, const int32_t* token_offset, const int32_t* leng
   p.nb = q8_blocks(Tcap, block_tokens);
   // L tokens touch the most blocks when they begin at a block's last token
   p.blocks = token_offset ? q8_blocks(L - 1, block_tokens) + 1 : q8_blocks(L, block_tokens);
+  // units of a sequence are counted in 32 bits: (block, stream, head) of a write, 8 elements of a read
+  if (static_cast<long long>(p.blocks) * n * Hkv > (1LL << 31) - 1024 ||
+      static_cast<long long>(L) * n * Hkv * (D / 8) > (1LL << 31) - 1024)
+    return HD_ERR_UNSUPPORTED;
+  p.div_hkv = FastDiv::by(static_cast<uint32_t>(Hkv));
+  p.div_n = FastDiv::by(static_cast<uint32_t>(n));
+  p.div_bt = FastDiv::by(static_cast<uint32_t>(block_tokens));
   p.ext_rows = static_cast<long long>(B) * L * n * Hkv * D;
   p.ext_codes = static_cast<long long>(B) * Tcap * n * Hkv * D;
   p.ext_scale = static_cast<long long>(B) * Hkv * p.nb * n;
@@ -587,7 +594,7 @@ int hd_kv_write_q8(const void* k, const void* v, const int32_t* token_offset, co
   if (!aligned16(k) || !aligned16(v)) return HD_ERR_INVALID_ARG;
   p.k = static_cast<const __nv_bfloat16*>(k);
   p.v = static_cast<const __nv_bfloat16*>(v);
-  return from_cuda(launch_kv_write_q8(p, sm_count(), static_cast<cudaStream_t>(stream)));
+  return from_cuda(launch_kv_write_q8(p, static_cast<cudaStream_t>(stream)));
 }
 
 int hd_kv_read_q8(const void* k_codes, const void* v_codes, const float* k_scale, const float* v_scale,
@@ -602,7 +609,7 @@ int hd_kv_read_q8(const void* k_codes, const void* v_codes, const float* k_scale
   if (!aligned16(k) || !aligned16(v)) return HD_ERR_INVALID_ARG;
   p.k_out = static_cast<__nv_bfloat16*>(k);
   p.v_out = static_cast<__nv_bfloat16*>(v);
-  return from_cuda(launch_kv_read_q8(p, sm_count(), static_cast<cudaStream_t>(stream)));
+  return from_cuda(launch_kv_read_q8(p, static_cast<cudaStream_t>(stream)));
 }
 
 size_t hd_decode_q8_workspace_bytes(int B, int n, int Tcap, int Hq, int Hkv, int D) {

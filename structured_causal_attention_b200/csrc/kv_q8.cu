@@ -19,10 +19,12 @@
 // are then rounded again; it is never lowered, so nothing is rounded twice
 // unless the range grew.
 //
-// One warp owns one (K or V, sequence, block, stream, head): it alone reads
-// and writes that scale and those codes, so no atomics and no order between
-// warps. Rows of neighbouring heads are neighbours in memory and so are their
-// warps.
+// Writing: one warp owns one (K or V, sequence, block, stream, head): it alone
+// reads and writes that scale and those codes, so no atomics and no order
+// between warps. It holds its block's rows in registers between finding their
+// largest magnitude and storing their codes, so each row is read once. Rows of
+// neighbouring heads are neighbours in memory and so are their warps.
+// Reading: eight codes a thread, four such in flight.
 #include <cuda_fp8.h>
 
 #include "hd_common.cuh"
@@ -48,14 +50,18 @@ __device__ __forceinline__ float scale_for(uint32_t abits) {
   return fmaxf(up, __int_as_float((kQ8MinExp + 127) << 23));
 }
 
-// Four bf16 values (two registers) over the scale, as four codes.
+// Two bf16 values (one register) over the scale.
+__device__ __forceinline__ float2 scaled(uint32_t x, float inv) {
+  return make_float2(__uint_as_float(x << 16) * inv, __uint_as_float(x & 0xffff0000u) * inv);
+}
+
+// Four bf16 values over the scale, as four codes.
 template <int FMT>
-__device__ __forceinline__ uint32_t quantise4(uint2 x, float inv) {
-  const float f0 = __uint_as_float(x.x << 16) * inv, f1 = __uint_as_float(x.x & 0xffff0000u) * inv;
-  const float f2 = __uint_as_float(x.y << 16) * inv, f3 = __uint_as_float(x.y & 0xffff0000u) * inv;
+__device__ __forceinline__ uint32_t quantise4(uint32_t x0, uint32_t x1, float inv) {
+  const float2 f = scaled(x0, inv), g = scaled(x1, inv);
   if (FMT == HD_Q8_E4M3) {
-    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(f0, f1), __NV_SATFINITE, __NV_E4M3);
-    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(f2, f3), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(g, __NV_SATFINITE, __NV_E4M3);
     return lo | (hi << 16);
   }
   // x * (1/scale) is within 2^-15 of x / scale. Rounding it to a multiple of
@@ -63,8 +69,8 @@ __device__ __forceinline__ uint32_t quantise4(uint2 x, float inv) {
   // moves no other value across one; adding 1.5 * 2^23 then leaves the nearest
   // even integer in the low bits.
   const float c = 1.5f * (1 << 11), d = 1.5f * (1 << 23);
-  const uint32_t i0 = __float_as_uint(((f0 + c) - c) + d), i1 = __float_as_uint(((f1 + c) - c) + d);
-  const uint32_t i2 = __float_as_uint(((f2 + c) - c) + d), i3 = __float_as_uint(((f3 + c) - c) + d);
+  const uint32_t i0 = __float_as_uint(((f.x + c) - c) + d), i1 = __float_as_uint(((f.y + c) - c) + d);
+  const uint32_t i2 = __float_as_uint(((g.x + c) - c) + d), i3 = __float_as_uint(((g.y + c) - c) + d);
   return __byte_perm(__byte_perm(i0, i1, 0x0040), __byte_perm(i2, i3, 0x0040), 0x5410);
 }
 
@@ -75,6 +81,14 @@ __device__ __forceinline__ float code_value(uint32_t c) {
     return __half2float(__half(h));
   }
   return static_cast<float>(static_cast<int8_t>(c));
+}
+
+// The codes in the two low bytes.
+template <int FMT>
+__device__ __forceinline__ float2 code_pair(uint32_t c) {
+  if (FMT == HD_Q8_E4M3)
+    return __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(c & 0xffffu), __NV_E4M3)));
+  return make_float2(code_value<FMT>(c & 0xffu), code_value<FMT>((c >> 8) & 0xffu));
 }
 
 // Four codes again at a larger scale: rn(code * old / now).
@@ -101,144 +115,173 @@ __device__ __forceinline__ bool token_range(const KvQ8Params& p, int b, int& t0,
   return false;
 }
 
-template <int D, int FMT>
+// NP: passes (of 32 * 8 / D rows) held in registers; longer blocks are read a
+// second time for their codes.
+template <int D, int FMT, int NP>
 __global__ void __launch_bounds__(kKvWarps * 32) kv_write_q8_kernel(const KvQ8Params p) {
-  constexpr int LPR = D / 4;      // lanes of a row, four elements each
+  constexpr int LPR = D / 8;      // lanes of a row, eight elements each
   constexpr int RPP = 32 / LPR;   // rows of a pass
-  const int lane = threadIdx.x & 31, sub = lane / LPR, col = (lane % LPR) * 4;
-  const long long warps = static_cast<long long>(gridDim.x) * kKvWarps;
-  const long long per_tensor = static_cast<long long>(p.B) * p.blocks * p.n * p.Hkv;
-  for (long long u = static_cast<long long>(blockIdx.x) * kKvWarps + (threadIdx.x >> 5); u < 2 * per_tensor;
-       u += warps) {
-    long long i = u;
-    const int hk = static_cast<int>(i % p.Hkv);
-    i /= p.Hkv;
-    const int s = static_cast<int>(i % p.n);
-    i /= p.n;
-    const int jb = static_cast<int>(i % p.blocks);
-    i /= p.blocks;
-    const int b = static_cast<int>(i % p.B);
-    const bool is_v = i >= p.B;
+  const int lane = threadIdx.x & 31, sub = lane / LPR, col = (lane % LPR) * 8;
+  const bool is_v = blockIdx.z != 0;
+  const __nv_bfloat16* x = is_v ? p.v : p.k;
+  uint8_t* codes = is_v ? p.v_codes : p.k_codes;
+  float* scales = is_v ? p.v_scale : p.k_scale;
+  const uint32_t unit = blockIdx.x * kKvWarps + (threadIdx.x >> 5);
+  const uint32_t bs = p.div_hkv.div(unit);
+  const int hk = static_cast<int>(unit - bs * p.Hkv);
+  const int jb = static_cast<int>(p.div_n.div(bs));
+  const int s = static_cast<int>(bs) - jb * p.n;
+  if (jb >= p.blocks) return;
+  for (int b = blockIdx.y; b < p.B; b += gridDim.y) {
     int t0, len;
     if (!token_range(p, b, t0, len, lane == 0 && jb == 0) || len == 0) continue;
-    const int blk = t0 / p.bt + jb;
-    const long long first = static_cast<long long>(blk) * p.bt;   // the block's first token
-    const long long end = min(first + p.bt, static_cast<long long>(t0) + len);
-    const long long lo = max(first, static_cast<long long>(t0));  // new rows: tokens lo .. end-1
+    const int blk = static_cast<int>(p.div_bt.div(t0)) + jb;
+    const long long first = static_cast<long long>(blk) * p.bt;  // the block's first token
+    const int end = static_cast<int>(min(first + p.bt, static_cast<long long>(t0) + len));
+    const int lo = static_cast<int>(max(first, static_cast<long long>(t0)));  // new rows: tokens lo .. end-1
     if (lo >= end) continue;
-    const __nv_bfloat16* x = is_v ? p.v : p.k;
-    uint8_t* codes = is_v ? p.v_codes : p.k_codes;
-    const long long xrow = static_cast<long long>(p.n) * p.Hkv * D;  // elements of a token
-    const long long xo = (static_cast<long long>(b) * p.L - t0) * xrow + (static_cast<long long>(s) * p.Hkv + hk) * D + col;
-    const long long co = static_cast<long long>(b) * p.Tcap * xrow + (static_cast<long long>(s) * p.Hkv + hk) * D + col;
+    const long long tstep = static_cast<long long>(p.n) * p.Hkv * D;  // elements of a token
+    const long long at = (static_cast<long long>(s) * p.Hkv + hk) * D + col;
+    const long long xo = (static_cast<long long>(b) * p.L - t0) * tstep + at;
+    const long long co = static_cast<long long>(b) * p.Tcap * tstep + at;
     const long long si = ((static_cast<long long>(b) * p.Hkv + hk) * p.nb + blk) * p.n + s;
-    float* scale_ptr = (is_v ? p.v_scale : p.k_scale) + si;
     if (!in_bounds(si, 1, p.ext_scale, p.status)) continue;
-
-    uint32_t am = 0;  // largest magnitude, as two bf16 halves
-    for (long long t = lo + sub; t < end; t += RPP) {
-      const long long o = xo + t * xrow;
-      if (!in_bounds(o, 4, p.ext_rows, p.status)) continue;
-      const uint2 r = __ldg(reinterpret_cast<const uint2*>(x + o));
-      am = __vmaxu2(am, __vmaxu2(r.x & 0x7fff7fffu, r.y & 0x7fff7fffu));
-    }
+    auto row = [&](int t) {
+      const long long o = xo + t * tstep;
+      if (t >= end || !in_bounds(o, 8, p.ext_rows, p.status)) return make_uint4(0, 0, 0, 0);
+      return __ldg(reinterpret_cast<const uint4*>(x + o));
+    };
+    auto largest = [](uint32_t am, const uint4& r) {  // of magnitudes, as two bf16 halves
+      const uint32_t u = __vmaxu2(r.x & 0x7fff7fffu, r.y & 0x7fff7fffu);
+      const uint32_t v = __vmaxu2(r.z & 0x7fff7fffu, r.w & 0x7fff7fffu);
+      return __vmaxu2(am, __vmaxu2(u, v));
+    };
+    const float old = first < t0 ? scales[si] : 0.f;
+    uint4 held[NP];
+    uint32_t am = 0;
+#pragma unroll
+    for (int i = 0; i < NP; ++i) held[i] = row(lo + sub + i * RPP);
+#pragma unroll
+    for (int i = 0; i < NP; ++i) am = largest(am, held[i]);
+    for (int t = lo + sub + NP * RPP; t < end; t += RPP) am = largest(am, row(t));
     const uint32_t abits = __reduce_max_sync(0xffffffffu, max(am & 0xffffu, am >> 16));
     const bool finite = abits < 0x7f80u;
-    const float old = first < t0 ? *scale_ptr : 0.f;
-    __syncwarp();  // every lane has read the old scale before lane 0 replaces it
     float now = finite ? fmaxf(scale_for<FMT>(abits), old) : __int_as_float(0x7fffffff);
     if (old != old) now = old;
     const bool poison = now != now;
-    if (lane == 0) *scale_ptr = now;
+    if (lane == 0) scales[si] = now;  // every lane's read of the old one is before the reduction
     if (first < t0 && now > old) {
-      for (long long t = first + sub; t < lo; t += RPP) {
-        const long long o = co + t * xrow;
-        if (!in_bounds(o, 4, p.ext_codes, p.status)) continue;
-        uint32_t* c = reinterpret_cast<uint32_t*>(codes + o);
-        *c = requantise4<FMT>(*c, old, now);
+      for (int t = static_cast<int>(first) + sub; t < lo; t += RPP) {
+        const long long o = co + t * tstep;
+        if (!in_bounds(o, 8, p.ext_codes, p.status)) continue;
+        uint2* c = reinterpret_cast<uint2*>(codes + o);
+        const uint2 was = *c;
+        *c = make_uint2(requantise4<FMT>(was.x, old, now), requantise4<FMT>(was.y, old, now));
       }
     }
     const float inv = __fdiv_rn(1.f, now);
-    for (long long t = lo + sub; t < end; t += RPP) {
-      const long long o = xo + t * xrow, w = co + t * xrow;
-      if (!in_bounds(o, 4, p.ext_rows, p.status) || !in_bounds(w, 4, p.ext_codes, p.status)) continue;
-      const uint2 r = __ldg(reinterpret_cast<const uint2*>(x + o));
-      *reinterpret_cast<uint32_t*>(codes + w) = poison ? 0u : quantise4<FMT>(r, inv);
-    }
+    auto store = [&](int t, const uint4& r) {
+      const long long o = co + t * tstep;
+      if (t >= end || !in_bounds(o, 8, p.ext_codes, p.status)) return;
+      *reinterpret_cast<uint2*>(codes + o) =
+          poison ? make_uint2(0, 0) : make_uint2(quantise4<FMT>(r.x, r.y, inv), quantise4<FMT>(r.z, r.w, inv));
+    };
+#pragma unroll
+    for (int i = 0; i < NP; ++i) store(lo + sub + i * RPP, held[i]);
+    for (int t = lo + sub + NP * RPP; t < end; t += RPP) store(t, row(t));
   }
 }
 
-// One thread a chunk of 8 codes: 8 bytes in, 16 bytes out.
 template <int D, int FMT>
 __global__ void __launch_bounds__(256) kv_read_q8_kernel(const KvQ8Params p) {
-  constexpr int CPR = D / 8;
-  const long long per_tensor = static_cast<long long>(p.B) * p.L * p.n * p.Hkv * CPR;
-  const long long threads = static_cast<long long>(gridDim.x) * blockDim.x;
-  for (long long u = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; u < 2 * per_tensor; u += threads) {
-    const bool is_v = u >= per_tensor;
-    const long long e = is_v ? u - per_tensor : u;  // chunk of the rows read
-    long long i = e;
-    const int ch = static_cast<int>(i % CPR);
-    i /= CPR;
-    const int hk = static_cast<int>(i % p.Hkv);
-    i /= p.Hkv;
-    const int s = static_cast<int>(i % p.n);
-    i /= p.n;
-    const int t = static_cast<int>(i % p.L);
-    const int b = static_cast<int>(i / p.L);
+  constexpr int CPR = D / 8, PER = 4;
+  const bool is_v = blockIdx.z != 0;
+  const uint8_t* codes = is_v ? p.v_codes : p.k_codes;
+  const float* scales = is_v ? p.v_scale : p.k_scale;
+  __nv_bfloat16* out = is_v ? p.v_out : p.k_out;
+  const uint32_t tchunks = static_cast<uint32_t>(p.n) * p.Hkv * CPR;  // chunks of a token
+  const uint32_t chunks = tchunks * p.L;                             // and of a sequence
+  for (int b = blockIdx.y; b < p.B; b += gridDim.y) {
     int t0, len;
-    if (!token_range(p, b, t0, len, t == 0 && ch == 0) || t >= len) continue;
-    const int tok = t0 + t;
-    const long long co = (((static_cast<long long>(b) * p.Tcap + tok) * p.n + s) * p.Hkv + hk) * D + ch * 8;
-    const long long si = ((static_cast<long long>(b) * p.Hkv + hk) * p.nb + tok / p.bt) * p.n + s;
-    if (!in_bounds(co, 8, p.ext_codes, p.status) || !in_bounds(si, 1, p.ext_scale, p.status) ||
-        !in_bounds(e * 8, 8, p.ext_rows, p.status))
-      continue;
-    const uint2 c = *reinterpret_cast<const uint2*>((is_v ? p.v_codes : p.k_codes) + co);
-    const float sc = (is_v ? p.v_scale : p.k_scale)[si];
-    uint32_t r[4];
+    if (!token_range(p, b, t0, len, threadIdx.x == 0 && blockIdx.x == 0)) len = 0;
+    uint2 c[PER];
+    float sc[PER];
+    const uint32_t e0 = blockIdx.x * (256 * PER) + threadIdx.x;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t w = (j < 2 ? c.x : c.y) >> ((j & 1) * 16);
-      r[j] = pack_bf16(code_value<FMT>(w & 0xffu) * sc, code_value<FMT>((w >> 8) & 0xffu) * sc);
+    for (int j = 0; j < PER; ++j) {
+      const uint32_t e = e0 + j * 256;
+      const uint32_t r = e / CPR;                       // (token, stream, head)
+      const uint32_t pos = p.div_hkv.div(r), hk = r - pos * p.Hkv;
+      const uint32_t t = p.div_n.div(pos), s = pos - t * p.n;
+      c[j] = make_uint2(0, 0);
+      sc[j] = 0.f;  // rows behind the sequence are zeros
+      if (e < chunks && static_cast<int>(t) < len) {
+        const uint32_t tok = t0 + t;
+        const long long co = (static_cast<long long>(b) * p.Tcap + t0) * tchunks * 8 + static_cast<long long>(e) * 8;
+        const long long si =
+            ((static_cast<long long>(b) * p.Hkv + hk) * p.nb + p.div_bt.div(tok)) * p.n + s;
+        if (in_bounds(co, 8, p.ext_codes, p.status) && in_bounds(si, 1, p.ext_scale, p.status)) {
+          c[j] = __ldg(reinterpret_cast<const uint2*>(codes + co));
+          sc[j] = __ldg(scales + si);
+        }
+      }
     }
-    *reinterpret_cast<uint4*>((is_v ? p.v_out : p.k_out) + e * 8) = make_uint4(r[0], r[1], r[2], r[3]);
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      const uint32_t e = e0 + j * 256;
+      const long long o = static_cast<long long>(b) * chunks * 8 + static_cast<long long>(e) * 8;
+      if (e >= chunks || !in_bounds(o, 8, p.ext_rows, p.status)) continue;
+      uint32_t r[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t w = (k < 2 ? c[j].x : c[j].y) >> ((k & 1) * 16);
+        const float2 f = code_pair<FMT>(w);
+        r[k] = pack_bf16(f.x * sc[j], f.y * sc[j]);
+      }
+      *reinterpret_cast<uint4*>(out + o) = make_uint4(r[0], r[1], r[2], r[3]);
+    }
   }
 }
 
+dim3 kv_grid(long long x, int B) {
+  return dim3(static_cast<unsigned>(x), static_cast<unsigned>(B < 65535 ? B : 65535), 2);
+}
+
 template <int D, int FMT>
-cudaError_t launch_write_d(const KvQ8Params& p, int sms, cudaStream_t stream) {
-  const long long units = 2LL * p.B * p.blocks * p.n * p.Hkv;
-  long long grid = (units + kKvWarps - 1) / kKvWarps;
-  const long long cap = static_cast<long long>(sms) * 8 * 16;
-  if (grid > cap) grid = cap;
-  kv_write_q8_kernel<D, FMT><<<static_cast<unsigned>(grid), kKvWarps * 32, 0, stream>>>(p);
+cudaError_t launch_write_d(const KvQ8Params& p, cudaStream_t stream) {
+  constexpr int RPP = 32 * 8 / D;
+  const dim3 grid = kv_grid((static_cast<long long>(p.blocks) * p.n * p.Hkv + kKvWarps - 1) / kKvWarps, p.B);
+  // rows of a block that can be new in one call
+  const int rows = p.bt < p.L ? p.bt : p.L;
+  if (rows <= 2 * RPP)
+    kv_write_q8_kernel<D, FMT, 2><<<grid, kKvWarps * 32, 0, stream>>>(p);
+  else if (rows <= 8 * RPP)
+    kv_write_q8_kernel<D, FMT, 8><<<grid, kKvWarps * 32, 0, stream>>>(p);
+  else
+    kv_write_q8_kernel<D, FMT, 16><<<grid, kKvWarps * 32, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
 template <int D, int FMT>
-cudaError_t launch_read_d(const KvQ8Params& p, int sms, cudaStream_t stream) {
-  const long long units = 2LL * p.B * p.L * p.n * p.Hkv * (D / 8);
-  long long grid = (units + 255) / 256;
-  const long long cap = static_cast<long long>(sms) * 8 * 16;
-  if (grid > cap) grid = cap;
-  kv_read_q8_kernel<D, FMT><<<static_cast<unsigned>(grid), 256, 0, stream>>>(p);
+cudaError_t launch_read_d(const KvQ8Params& p, cudaStream_t stream) {
+  const long long chunks = static_cast<long long>(p.L) * p.n * p.Hkv * (D / 8);
+  kv_read_q8_kernel<D, FMT><<<kv_grid((chunks + 1023) / 1024, p.B), 256, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_kv_write_q8(const KvQ8Params& p, int sms, cudaStream_t stream) {
+cudaError_t launch_kv_write_q8(const KvQ8Params& p, cudaStream_t stream) {
   const bool e4m3 = p.format == HD_Q8_E4M3;
-  if (p.D == 64) return e4m3 ? launch_write_d<64, HD_Q8_E4M3>(p, sms, stream) : launch_write_d<64, HD_Q8_INT8>(p, sms, stream);
-  if (p.D == 128) return e4m3 ? launch_write_d<128, HD_Q8_E4M3>(p, sms, stream) : launch_write_d<128, HD_Q8_INT8>(p, sms, stream);
+  if (p.D == 64) return e4m3 ? launch_write_d<64, HD_Q8_E4M3>(p, stream) : launch_write_d<64, HD_Q8_INT8>(p, stream);
+  if (p.D == 128) return e4m3 ? launch_write_d<128, HD_Q8_E4M3>(p, stream) : launch_write_d<128, HD_Q8_INT8>(p, stream);
   return cudaErrorInvalidValue;
 }
 
-cudaError_t launch_kv_read_q8(const KvQ8Params& p, int sms, cudaStream_t stream) {
+cudaError_t launch_kv_read_q8(const KvQ8Params& p, cudaStream_t stream) {
   const bool e4m3 = p.format == HD_Q8_E4M3;
-  if (p.D == 64) return e4m3 ? launch_read_d<64, HD_Q8_E4M3>(p, sms, stream) : launch_read_d<64, HD_Q8_INT8>(p, sms, stream);
-  if (p.D == 128) return e4m3 ? launch_read_d<128, HD_Q8_E4M3>(p, sms, stream) : launch_read_d<128, HD_Q8_INT8>(p, sms, stream);
+  if (p.D == 64) return e4m3 ? launch_read_d<64, HD_Q8_E4M3>(p, stream) : launch_read_d<64, HD_Q8_INT8>(p, stream);
+  if (p.D == 128) return e4m3 ? launch_read_d<128, HD_Q8_E4M3>(p, stream) : launch_read_d<128, HD_Q8_INT8>(p, stream);
   return cudaErrorInvalidValue;
 }
 

@@ -48,6 +48,25 @@ void decode_split_plan(int B, int rows, long long keys, int Hkv, int sms, int* m
                        int* chunk);
 cudaError_t launch_decode(const DecodeParams& p, cudaStream_t stream);
 
+// Division of numbers below 2^31 by a divisor known at launch: with
+// l = ceil(log2 d) and m = ceil(2^(31+l) / d), m is below 2^32 for d no power of
+// two, and x / d = floor(x m / 2^(31+l)) as x (m d - 2^(31+l)) < 2^31 d <= 2^(31+l).
+struct FastDiv {
+  uint32_t mul, shift;  // mul = 0: a power of two
+  static FastDiv by(uint32_t d) {
+    FastDiv f = {0, 0};
+    while ((1ull << f.shift) < d) ++f.shift;
+    if ((1ull << f.shift) == d) return f;
+    f.mul = static_cast<uint32_t>(((1ull << (31 + f.shift)) + d - 1) / d);
+    f.shift -= 1;
+    return f;
+  }
+  __host__ __device__ uint32_t div(uint32_t x) const {
+    if (mul == 0) return x >> shift;
+    return static_cast<uint32_t>((static_cast<unsigned long long>(x) * mul) >> 32) >> shift;
+  }
+};
+
 // The 8-bit KV cache: rows written to or read from tokens t0 .. t0+len-1 of each
 // sequence, t0 = token_offset[b] (or 0), len = lengths[b] (or L).
 constexpr int kQ8MinExp = -60;  // the smallest scale is 2^-60
@@ -65,11 +84,12 @@ struct KvQ8Params {
   int* status;
   int B, L, n, Tcap, Hkv, D, format, bt, nb;  // nb = blocks of bt tokens in Tcap
   int blocks;              // blocks that L tokens can touch
+  FastDiv div_hkv, div_n, div_bt;
   // allocated elements, for the checked build's bounds checks
   long long ext_rows, ext_codes, ext_scale;
 };
-cudaError_t launch_kv_write_q8(const KvQ8Params& p, int sms, cudaStream_t stream);
-cudaError_t launch_kv_read_q8(const KvQ8Params& p, int sms, cudaStream_t stream);
+cudaError_t launch_kv_write_q8(const KvQ8Params& p, cudaStream_t stream);
+cudaError_t launch_kv_read_q8(const KvQ8Params& p, cudaStream_t stream);
 
 // Decode attention over the 8-bit cache. The nq query streams s0 .. s0+nq-1 of
 // the new token are `groups` problems a KV head of spg streams each: under INTRA

@@ -79,15 +79,17 @@ def test_read_is_the_definitions(shape, fmt):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
-def test_read_leaves_rows_behind_a_sequence(fmt):
+def test_rows_behind_a_sequence_are_zeros(fmt):
     need_gpu()
-    B, L, n, Hkv, D = 3, 6, 2, 2, 64
-    cache = hd.kv_cache_q8(B, 10, n, Hkv, D, torch.int8 if fmt == "int8" else torch.float8_e4m3fn, 4)
-    out = tuple(torch.full((B, L * n, Hkv, D), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
-    hd.kv_read_q8(cache, L, _i32([0, 2, 4]), _i32([6, 0, 3]), out=out)
-    for t in out:
-        for b, m in enumerate([6, 0, 3]):
-            assert (t[b, :m * n] == 0).all() and (t[b, m * n:] == 7).all()
+    B, L, n, Hkv, D, bt = 3, 6, 2, 2, 64, 4
+    cache = garbage_cache(B, 10, n, Hkv, D, fmt, bt)
+    x = rows((B, 10 * n, Hkv, D), 1, n)
+    host = _write(cache, on_host(cache), x, x, fmt)
+    out = tuple(torch.full((B, L * n, Hkv, D), float("nan"), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    off, length = [0, 2, 4], [6, 0, 3]
+    hd.kv_read_q8(cache, L, _i32(off), _i32(length), out=out)
+    want = torch.tensor(oracle.kv_read_q8(*host["k"], n, bt, fmt, L, off, length), dtype=torch.float32).to(torch.bfloat16)
+    assert (want[1] == 0).all() and torch.equal(out[0].cpu(), want) and torch.equal(out[1].cpu(), want)
 
 
 @pytest.mark.parametrize("fmt", FMTS)
@@ -159,7 +161,7 @@ def test_a_range_outside_is_left_alone(off, length, bad):
     out = tuple(torch.full((B, L * n, Hkv, D), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
     hd.kv_read_q8(cache, L, _i32(off), _i32(length), out=out)
     assert hd.hd_device_status(clear=True) == hd.HD_ERR_DEVICE_INDEX
-    assert (out[0][bad] == 7).all() and (out[1][bad] == 7).all()
+    assert (out[0][bad] == 0).all() and (out[1][bad] == 0).all()
     want = oracle.kv_read_q8(*host["k"], n, bt, "int8", L, off, length)[good, :length[good] * n]
     assert torch.equal(out[0][good, :length[good] * n].cpu(), torch.tensor(want, dtype=torch.float32).to(torch.bfloat16))
 
