@@ -282,9 +282,12 @@ void decode_q8_problem(DecodeQ8Params& p, int mode, int W_tokens, int final_only
     // the first of nq queries begins its window nq - 1 positions before the last
     if (w + p.nq - 1 < keys) keys = w + p.nq - 1;
   }
-  p.rows = p.spg * (p.Hq / p.Hkv);
-  p.mt = (p.rows + 15) / 16;
-  decode_q8_plan(static_cast<long long>(p.B) * p.Hkv * p.groups * p.mt, keys, sm_count(), &p.splits, &p.chunk);
+  p.g = p.Hq / p.Hkv;
+  p.rows = p.spg * p.g;
+  p.tile_rows = decode_q8_tile_rows(p.rows);
+  p.mt = (p.rows + p.tile_rows - 1) / p.tile_rows;
+  decode_q8_plan(static_cast<long long>(p.B) * p.Hkv * p.groups * p.mt, keys, p.tile_rows, sm_count(), &p.splits,
+                 &p.chunk);
 }
 
 // The most that any mode needs of one decode step over the 8-bit cache.
@@ -300,8 +303,9 @@ size_t decode_q8_workspace(int B, int n, int Tcap, int Hq, int Hkv, int D, int f
     p.Hkv = Hkv;
     decode_q8_problem(p, mode, 1, final_only);
     const long long problems = static_cast<long long>(B) * Hkv * p.groups * p.mt;
-    const long long splits = decode_q8_most_splits(problems, static_cast<long long>(Tcap) * p.kpt, sm_count());
-    const size_t prow = static_cast<size_t>(problems) * 16 * static_cast<size_t>(splits);
+    const long long splits = decode_q8_most_splits(problems, static_cast<long long>(Tcap) * p.kpt, p.tile_rows,
+                                                   sm_count());
+    const size_t prow = static_cast<size_t>(problems) * p.tile_rows * static_cast<size_t>(splits);
     const size_t need = align256(prow * static_cast<size_t>(D) * 4) + align256(prow * 2 * 4);
     if (need > most) most = need;
   }
@@ -347,8 +351,21 @@ int decode_q8_call(const void* q, const void* k_codes, const void* v_codes, cons
   p.nb = q8_blocks(Tcap, block_tokens);
   p.scale_log2 = scale * 1.4426950408889634074f;
   decode_q8_problem(p, mode, W_tokens, final_only);
-  if (static_cast<long long>(B) * Hkv * p.groups * p.mt * p.splits > (1LL << 31) - 1) return HD_ERR_UNSUPPORTED;
-  const size_t prow = static_cast<size_t>(B) * Hkv * p.groups * p.mt * 16 * p.splits;
+  if (static_cast<long long>(B) * Hkv * p.groups * p.mt * p.splits * p.tile_rows > (1LL << 31) - 1) return HD_ERR_UNSUPPORTED;
+  const size_t prow = static_cast<size_t>(B) * Hkv * p.groups * p.mt * p.tile_rows * p.splits;
+  const bool intra = p.kpt == 1 && n > 1;
+  const int step_tok = intra ? kQ8Round : kQ8Round / n;
+  p.step_stream = intra ? 0 : kQ8Round % n;
+  p.step_blk = step_tok / p.bt;
+  p.step_off = step_tok % p.bt;
+  p.div_g = FastDiv::by(p.g);
+  p.div_mt = FastDiv::by(p.mt);
+  p.div_splits = FastDiv::by(p.splits);
+  p.div_groups = FastDiv::by(p.groups);
+  p.div_hkv = FastDiv::by(Hkv);
+  p.div_rows = FastDiv::by(p.rows);
+  p.div_n = FastDiv::by(n);
+  p.div_bt = FastDiv::by(p.bt);
   p.ext_q = static_cast<long long>(B) * p.nq * Hq * D;
   p.ext_lse = static_cast<long long>(B) * Hq * p.nq;
   p.ext_scale = static_cast<long long>(B) * Hkv * p.nb * n;

@@ -10,22 +10,21 @@
 //
 // Codes of both formats are exact in fp16, so the products run as fp16 MMAs on
 // converted codes and the scales stay outside, in fp32:
-//   - a query row is multiplied by the power of two that puts its largest
-//     magnitude in [2^14, 2^15): exact but for elements 2^29 and more below the
-//     largest, which keep an absolute error of 2^-40 of it;
-//   - with vs = 2^e * m, 1 <= m < 2, the weight of a key is w_j = 2^(s_j + e_j - M),
-//     s in log2 units. M follows the running maximum of s + e: it is set so that
-//     the largest weight is 2^13, and again once one passes 2^15, so that w_j m_j
-//     fits fp16 (rounding 2^-12, kept down to 2^-27 of the largest weight). The
-//     softmax's sum takes the same weights without the scale, l += w_j 2^-e_j, in
-//     fp32. So blocks of very different size need no common scale, and O / l
-//     needs no correction.
+//   - the query rows of a tile are multiplied by the power of two that puts the
+//     largest finite magnitude of them in [2^14, 2^15): exact but for elements
+//     2^29 and more below it, which keep an absolute error of 2^-40 of it;
+//   - the weight of a key is w_j = vs_j 2^(s_j - M), s in log2 units. M follows the
+//     running maximum of s + log2 vs: it is set so that the largest weight is
+//     2^13, and again once one passes 2^15, so that weights fit fp16 (rounding
+//     2^-12, kept down to 2^-27 of the largest). The softmax's sum takes the same
+//     weights without the scale, l += w_j / vs_j, in fp32. So blocks of very
+//     different size need no common scale, and O / l needs no correction.
 //
 // Under INTRA each stream is a problem of its own (g query rows, every n-th
 // position), so every loaded key is visible and none is read twice; otherwise
 // the n*g rows of a KV head share the keys. A CTA owns (sequence, KV head, stream
-// group, 16-row tile, chunk of keys); its warps each stream 32-key tiles of
-// their own through a TMA ring of their own, with nothing between warps until
+// group, tile of 16 RT rows, chunk of keys); its warps each stream 32-key tiles
+// of their own through a TMA ring of their own, with nothing between warps until
 // their states are merged at the end. The kernel writes the output itself where
 // one chunk holds the whole cache, else partials that a second kernel joins.
 #include <cuda_fp16.h>
@@ -42,17 +41,21 @@ namespace {
 constexpr int kQWarps = 4;
 constexpr int kQThreads = kQWarps * 32;
 constexpr int kQTile = 32;  // keys of a warp's tile
+static_assert(kQWarps * kQTile == kQ8Round, "a round");
 constexpr float kLn2 = 0.69314718055994530942f;
 
-template <int D>
+// RT row tiles of 16 a CTA: the codes are converted once for all of them.
+template <int D, int RT>
 struct Q8Smem {
+  static constexpr int CTAS = RT == 1 ? 3 : 2;       // resident on an SM
   static constexpr int KV = kQTile * D;              // bytes of K (or V) of a tile
-  static constexpr int STAGES = D == 128 ? 3 : 6;    // ~98 KB a CTA, two CTAs an SM
+  static constexpr int STAGES = (RT == 1 ? 2 : 3) * (128 / D);
   static constexpr int RING = kQWarps * STAGES * 2 * KV;
-  static constexpr int FAC = kQWarps * kQTile * 16;  // per warp and key: ks, e, 2^-e, m
-  static constexpr int MERGE = kQWarps * 16 * (D + 4) * 4;
+  static constexpr int Q = RT * 16 * D * 2;          // the query rows in fp16
+  static constexpr int FAC = kQWarps * kQTile * 12;  // per warp and key: score factor, log2 vs, 1/vs
+  static constexpr int MERGE = kQWarps * RT * 16 * (D + 4) * 4;
   static constexpr int BARS = kQWarps * STAGES * 8;
-  static constexpr int TOTAL = RING + FAC + BARS + 16 + 1024;  // and the alignment of the ring
+  static constexpr int TOTAL = RING + Q + FAC + BARS + 32 + 1024;  // and the alignment of the ring
   static_assert(MERGE <= RING, "merge buffer");
 };
 
@@ -99,38 +102,61 @@ __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+__device__ __forceinline__ uint64_t f32x2_fma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t f32x2_add(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float2 f32x2_parts(uint64_t a) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(a));
+  return f;
+}
+__device__ __forceinline__ uint64_t lds64(uint32_t addr) {
+  uint64_t r;
+  asm volatile("ld.shared.b64 %0, [%1];" : "=l"(r) : "r"(addr));
+  return r;
+}
+
 // Row `row` of a stream group: its stream (of the nq), and query head.
 struct QRow {
   int s, h;
 };
 __device__ __forceinline__ QRow q_row(const DecodeQ8Params& p, int grp, int hk, int row) {
-  const int g = p.Hq / p.Hkv;
-  return {grp * p.spg + row / g, hk * g + row % g};
+  const int sg = static_cast<int>(p.div_g.div(row));
+  return {grp * p.spg + sg, hk * p.g + row - sg * p.g};
 }
 
-template <int D, int FMT>
-__global__ void __launch_bounds__(kQThreads, 2)
+template <int D, int FMT, int RT>
+__global__ void __launch_bounds__(kQThreads, Q8Smem<D, RT>::CTAS)
     decode_q8_split_kernel(const DecodeQ8Params p, const __grid_constant__ CUtensorMap tmK,
                            const __grid_constant__ CUtensorMap tmV) {
-  using SM = Q8Smem<D>;
-  constexpr int S = SM::STAGES;
+  using SM = Q8Smem<D, RT>;
+  constexpr int S = SM::STAGES, ROWS = 16 * RT, RCQ = D / 8;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  const uint32_t sRing = smem_u32(smem);
+  const uint32_t sRing = smem_u32(smem), sQ = sRing + SM::RING;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + SM::RING + SM::FAC + SM::BARS);
-  long long idx = blockIdx.x;
-  const int mt = static_cast<int>(idx % p.mt);
-  idx /= p.mt;
-  const int split = static_cast<int>(idx % p.splits);
-  idx /= p.splits;
-  const int grp = static_cast<int>(idx % p.groups);
-  idx /= p.groups;
-  const int hk = static_cast<int>(idx % p.Hkv);
-  const int b = static_cast<int>(idx / p.Hkv);
+  int* after = reinterpret_cast<int*>(smem + SM::RING + SM::Q + SM::FAC + SM::BARS);
+  volatile int* abort_flag = after;
+  uint32_t idx = blockIdx.x, rest = p.div_mt.div(idx);
+  const int mt = static_cast<int>(idx - rest * p.mt);
+  idx = rest;
+  rest = p.div_splits.div(idx);
+  const int split = static_cast<int>(idx - rest * p.splits);
+  const uint32_t prob = rest;  // (sequence, KV head, group)
+  rest = p.div_groups.div(prob);
+  const int grp = static_cast<int>(prob - rest * p.groups);
+  const int b = static_cast<int>(p.div_hkv.div(rest));
+  const int hk = static_cast<int>(rest) - b * p.Hkv;
 
-  const int T1 = p.seqlen[b];
+  const int T1 = __ldg(p.seqlen + b);
   const bool ok = T1 >= 1 && T1 <= p.Tcap;
   if (!ok && tid == 0 && mt == 0 && split == 0 && grp == 0 && hk == 0) record_status(p.status, HD_ERR_DEVICE_INDEX);
   const int T = ok ? T1 - 1 : 0;
@@ -141,18 +167,16 @@ __global__ void __launch_bounds__(kQThreads, 2)
   const int kbeg = max(0, pmin - p.win + 1);      // (win is beyond any cache where there is none)
   const int cs = kbeg + split * p.chunk;
   const int ce = min(kend, cs + p.chunk);
-  const long long part_row0 = ((static_cast<long long>(b) * p.Hkv + hk) * p.groups + grp) * p.mt * 16 + mt * 16;
+  const int row0 = mt * ROWS, valid_rows = min(ROWS, p.rows - row0);
+  const long long part_row0 = static_cast<long long>(prob) * p.mt * ROWS + row0;
 
   if (cs >= ce) {  // nothing to read in this chunk
-    if (tid < 16) {
+    if (tid < valid_rows) {
       if (p.splits > 1) {
-        if (in_bounds((part_row0 + tid) * p.splits + split, 1, p.ext_part, p.status)) {
-          float* ml = p.part_ml + ((part_row0 + tid) * p.splits + split) * 2;
-          ml[0] = -INFINITY;
-          ml[1] = 0.f;
-        }
-      } else if (mt * 16 + tid < p.rows) {  // no sequence at all: a row of zeros
-        const QRow r = q_row(p, grp, hk, mt * 16 + tid);
+        if (in_bounds((part_row0 + tid) * p.splits + split, 1, p.ext_part, p.status))
+          reinterpret_cast<float2*>(p.part_ml)[(part_row0 + tid) * p.splits + split] = make_float2(-INFINITY, 0.f);
+      } else {  // no sequence at all: a row of zeros
+        const QRow r = q_row(p, grp, hk, row0 + tid);
         const long long oi = ((static_cast<long long>(b) * p.nq + r.s) * p.Hq + r.h) * D;
         const long long li = (static_cast<long long>(b) * p.Hq + r.h) * p.nq + r.s;
         if (in_bounds(oi, D, p.ext_q, p.status) && in_bounds(li, 1, p.ext_lse, p.status)) {
@@ -168,7 +192,7 @@ __global__ void __launch_bounds__(kQThreads, 2)
   const int all_tiles = (ce - cs + kQTile - 1) / kQTile;
   const int tiles = (all_tiles - warp + kQWarps - 1) / kQWarps;
   const uint32_t ring = sRing + warp * S * 2 * SM::KV;
-  const uint32_t bars = sRing + SM::RING + SM::FAC + warp * S * 8;
+  const uint32_t bars = sQ + SM::Q + SM::FAC + warp * S * 8;
   const int col = intra ? (p.s0 + grp) * p.Hkv + hk : hk;
   auto load = [&](int i) {
     const uint32_t bar = bars + (i % S) * 8, dst = ring + (i % S) * 2 * SM::KV;
@@ -184,18 +208,14 @@ __global__ void __launch_bounds__(kQThreads, 2)
     tc::fence_async_smem();
     for (int i = 0; i < S && i < tiles; ++i) load(i);
   }
-  __syncthreads();
 
   // ---- the scales: lane i has key i of the tile. Its place (block, token in the
   // block, stream) moves on by kQWarps tiles a step, without a division.
   const long long sc0 = (static_cast<long long>(b) * p.Hkv + hk) * p.nb * p.n;
   int key = cs + warp * kQTile + lane;
-  int stream = intra ? p.s0 + grp : key % p.n;
-  int tok = intra ? key : key / p.n;
-  int blk = tok / p.bt, off = tok - blk * p.bt;
-  const int step_stream = intra ? 0 : (kQWarps * kQTile) % p.n;
-  const int step_tok = intra ? kQWarps * kQTile : kQWarps * kQTile / p.n;
-  const int step_blk = step_tok / p.bt, step_off = step_tok - step_blk * p.bt;
+  int tok = intra ? key : static_cast<int>(p.div_n.div(key));
+  int stream = intra ? p.s0 + grp : key - tok * p.n;
+  int blk = static_cast<int>(p.div_bt.div(tok)), off = tok - blk * p.bt;
   float ks = 0.f, vs = 1.f;
   auto fetch_scales = [&]() {
     ks = 0.f;
@@ -206,9 +226,9 @@ __global__ void __launch_bounds__(kQThreads, 2)
       vs = __ldg(p.vs + si);
     }
     key += kQWarps * kQTile;
-    blk += step_blk;
-    off += step_off;
-    stream += step_stream;
+    blk += p.step_blk;
+    off += p.step_off;
+    stream += p.step_stream;
     if (stream >= p.n) {
       stream -= p.n;
       ++off;
@@ -220,66 +240,78 @@ __global__ void __launch_bounds__(kQThreads, 2)
   };
   fetch_scales();
 
-  // ---- Q: rows lane/4 and lane/4 + 8 of the tile. A register of an MMA's B
-  // operand holds four codes in a row of a key; so the k index 2t, 2t+1, 2t+8,
-  // 2t+9 of a step stands for d = 4t .. 4t+3 of its 16.
-  int prow[2];
-  float rfac[2];  // score factor of the row: scale * log2(e) over the row's power of two
-  uint32_t qf[D / 16][4];
-#pragma unroll
-  for (int hr = 0; hr < 2; ++hr) {
-    const int row = mt * 16 + (lane >> 2) + hr * 8;
-    const bool valid = row < p.rows;  // other rows are zeros, and are not written
-    const QRow qr = q_row(p, grp, hk, valid ? row : 0);
-    prow[hr] = intra ? T : T * p.n + p.s0 + qr.s;
-    const long long qi = ((static_cast<long long>(b) * p.nq + qr.s) * p.Hq + qr.h) * D;
-    const bool inb = in_bounds(qi, D, p.ext_q, p.status);
-    uint2 r[D / 16];
+  // ---- Q, as fp16 rows in shared memory. A register of an MMA's B operand holds
+  // four codes in a row of a key; so of the 16 k indexes of a step 2t, 2t+1, 2t+8,
+  // 2t+9 stand for d = 4t .. 4t+3.
+  float kfac;  // score factor: scale * log2(e) over the tile's power of two
+  {
+    constexpr int PER = ROWS * (D / 4) / kQThreads;
+    uint2 r[PER];
     uint32_t am = 0;
 #pragma unroll
-    for (int kk = 0; kk < D / 16; ++kk) {
-      r[kk] = (valid && inb) ? __ldg(reinterpret_cast<const uint2*>(p.q + qi + kk * 16 + (lane & 3) * 4))
-                             : make_uint2(0, 0);
-      am = __vmaxu2(am, __vmaxu2(r[kk].x & 0x7fff7fffu, r[kk].y & 0x7fff7fffu));
+    for (int i = 0; i < PER; ++i) {
+      const int lr = (tid + i * kQThreads) / (D / 4), d4 = (tid + i * kQThreads) % (D / 4);
+      r[i] = make_uint2(0, 0);  // rows past the last are zeros, and are not written
+      if (lr < valid_rows) {
+        const QRow qr = q_row(p, grp, hk, row0 + lr);
+        const long long qi = ((static_cast<long long>(b) * p.nq + qr.s) * p.Hq + qr.h) * D + d4 * 4;
+        if (in_bounds(qi, 4, p.ext_q, p.status)) r[i] = __ldg(reinterpret_cast<const uint2*>(p.q + qi));
+      }
+      const uint32_t u = r[i].x & 0x7fff7fffu, v = r[i].y & 0x7fff7fffu;
+      am = __vmaxu2(am, __vmaxu2(u & __vcmpltu2(u, 0x7f807f80u), v & __vcmpltu2(v, 0x7f807f80u)));
     }
-    am = max(am & 0xffffu, am >> 16);
-    am = max(am, __shfl_xor_sync(0xffffffffu, am, 1));
-    am = max(am, __shfl_xor_sync(0xffffffffu, am, 2));
-    // exponent of the row's largest magnitude; an infinity or NaN stays one
+    am = __reduce_max_sync(0xffffffffu, max(am & 0xffffu, am >> 16));
+    if (lane == 0) after[1 + warp] = static_cast<int>(am);
+    __syncthreads();
+    am = 0;
+#pragma unroll
+    for (int w = 0; w < kQWarps; ++w) am = max(am, static_cast<uint32_t>(after[1 + w]));
     const int e = max(static_cast<int>(am >> 7), 1) - 127;
     const int up = min(max(14 - e, -126), 126);
     const float f = __int_as_float((up + 127) << 23);
-    rfac[hr] = p.scale_log2 * __int_as_float((127 - up) << 23);
+    kfac = p.scale_log2 * __int_as_float((127 - up) << 23);
 #pragma unroll
-    for (int kk = 0; kk < D / 16; ++kk) {
-      qf[kk][hr] = pack_half(__uint_as_float(r[kk].x << 16) * f, __uint_as_float(r[kk].x & 0xffff0000u) * f);
-      qf[kk][2 + hr] = pack_half(__uint_as_float(r[kk].y << 16) * f, __uint_as_float(r[kk].y & 0xffff0000u) * f);
+    for (int i = 0; i < PER; ++i) {
+      const int lr = (tid + i * kQThreads) / (D / 4), d4 = (tid + i * kQThreads) % (D / 4);
+      const uint32_t lo = pack_half(__uint_as_float(r[i].x << 16) * f, __uint_as_float(r[i].x & 0xffff0000u) * f);
+      const uint32_t hi = pack_half(__uint_as_float(r[i].y << 16) * f, __uint_as_float(r[i].y & 0xffff0000u) * f);
+      const uint32_t at = (d4 & 3) * 4;
+      asm volatile("st.shared.b32 [%0], %1;\n" ::"r"(sQ + swz(lr, (d4 >> 2) * 2, RCQ) + at), "r"(lo) : "memory");
+      asm volatile("st.shared.b32 [%0], %1;\n" ::"r"(sQ + swz(lr, (d4 >> 2) * 2 + 1, RCQ) + at), "r"(hi) : "memory");
     }
+    __syncthreads();
   }
-  // o[c][h]: d = c*16 + 4t + h and + 2 + h (h = 0, 1) of rows lane/4, lane/4 + 8
-  float o[D / 16][2][4];
-#pragma unroll
-  for (int c = 0; c < D / 16; ++c)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) o[c][0][e] = o[c][1][e] = 0.f;
-  float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
 
-  float4* fac = reinterpret_cast<float4*>(smem + SM::RING) + warp * kQTile;
+  // o[rt][c][h]: d = c*16 + 4t + h and + 2 + h (h = 0, 1) of rows lane/4, lane/4 + 8
+  float o[RT][D / 16][2][4];
+  float m_run[RT][2];
+  uint64_t l_run[RT][2];  // two partial sums a row
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[rt][c][0][e] = o[rt][c][1][e] = 0.f;
+    m_run[rt][0] = m_run[rt][1] = -INFINITY;
+    l_run[rt][0] = l_run[rt][1] = 0;
+  }
+  const uint32_t sFac = sQ + SM::Q + warp * (kQTile * 12);
+  float* fac = reinterpret_cast<float*>(smem + SM::RING + SM::Q) + warp * (kQTile * 3);
   int done = 0;  // tiles whose copies have arrived
   for (; done < tiles; ++done) {
     const int st = done % S;
     const int base = cs + (done * kQWarps + warp) * kQTile;
     const uint32_t kb = ring + st * 2 * SM::KV, vb = kb + SM::KV;
-    __syncwarp();
     {
       const uint32_t vbits = __float_as_uint(vs);
       const int e = static_cast<int>((vbits >> 23) & 0xffu) - 127;
       const bool fin = e < 128 && e > -127;
       // A scale that is no number (its block took in one) makes the scores of its
-      // visible keys NaN. One of zero (never written) is the smallest, of zeros.
-      fac[lane] = make_float4(ks, e == 128 ? __int_as_float(0x7fffffff) : static_cast<float>(fin ? e : kQ8MinExp),
-                              __int_as_float((127 - (fin ? e : (e == 128 ? 0 : kQ8MinExp))) << 23),
-                              fin ? __uint_as_float((vbits & 0x007fffffu) | 0x3f800000u) : 0.f);
+      // visible keys NaN. One of zero (never written) counts as the smallest.
+      fac[lane] = ks * kfac;
+      fac[kQTile + lane] = fin ? static_cast<float>(e) + __log2f(__uint_as_float((vbits & 0x007fffffu) | 0x3f800000u))
+                               : (e == 128 ? __int_as_float(0x7fffffff) : static_cast<float>(kQ8MinExp));
+      fac[2 * kQTile + lane] = fin ? __fdividef(1.f, vs) : (e == 128 ? 1.f : __int_as_float((127 - kQ8MinExp) << 23));
     }
     fetch_scales();  // of the next tile
     if (!tc::mbar_wait_warp(bars + st * 8, (done / S) & 1, abort_flag, p.status)) break;
@@ -292,70 +324,99 @@ __global__ void __launch_bounds__(kQThreads, 2)
     }
     __syncwarp();
 
-    float s[kQTile / 8][4];
+    float s[RT][kQTile / 8][4];
 #pragma unroll
-    for (int j = 0; j < kQTile / 8; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
+    for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-    for (int c4 = 0; c4 < D / 16; c4 += 4)
+      for (int j = 0; j < kQTile / 8; ++j) s[rt][j][0] = s[rt][j][1] = s[rt][j][2] = s[rt][j][3] = 0.f;
 #pragma unroll
-      for (int j = 0; j < kQTile / 8; ++j) {  // 8 keys, 64 of d
-        uint32_t r[4];
-        ldsm_x4(kb + swz8<D>(j * 8 + (lane & 7), c4 + (lane >> 3)), r[0], r[1], r[2], r[3]);
+    for (int c4 = 0; c4 < D / 16; c4 += 4) {
+      uint32_t r[kQTile / 8][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+      for (int j = 0; j < kQTile / 8; ++j)  // 8 keys, 64 of d
+        ldsm_x4(kb + swz8<D>(j * 8 + (lane & 7), c4 + (lane >> 3)), r[j][0], r[j][1], r[j][2], r[j][3]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t qf[RT][4];
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+          ldsm_x4(sQ + swz(rt * 16 + (lane & 15), (c4 + i) * 2 + (lane >> 4), RCQ), qf[rt][0], qf[rt][1], qf[rt][2],
+                  qf[rt][3]);
+#pragma unroll
+        for (int j = 0; j < kQTile / 8; ++j) {
           uint32_t b0, b1;
-          to_half<FMT, true>(r[i], b0, b1);
-          mma_f16_16816(s[j], qf[c4 + i], b0, b1);
-        }
-      }
-    float mx[2] = {-INFINITY, -INFINITY};
-    const bool all_seen = base + kQTile <= ce && base + kQTile - 1 <= pmin && pmax - base < p.win;
+          to_half<FMT, true>(r[j][i], b0, b1);
 #pragma unroll
-    for (int j = 0; j < kQTile / 8; ++j)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int k = j * 8 + (lane & 3) * 2 + e;
-        const float2 f = *reinterpret_cast<const float2*>(fac + k);
-#pragma unroll
-        for (int hr = 0; hr < 2; ++hr) {
-          float& x = s[j][2 * hr + e];
-          x = fmaf(x, f.x * rfac[hr], f.y);
-          const int c = base + k;
-          if (!all_seen && !(c < ce && c <= prow[hr] && prow[hr] - c < p.win)) x = -INFINITY;
-          mx[hr] = fmaxf(mx[hr], x);
-        }
-      }
-    if (__any_sync(0xffffffffu, mx[0] > m_run[0] + 15.f || mx[1] > m_run[1] + 15.f)) {
-#pragma unroll
-      for (int hr = 0; hr < 2; ++hr) {
-        float m = fmaxf(mx[hr], __shfl_xor_sync(0xffffffffu, mx[hr], 1));
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-        if (m > m_run[hr] + 15.f) {
-          const float alpha = fast_exp2(m_run[hr] - (m - 13.f));
-          m_run[hr] = m - 13.f;
-          l_run[hr] *= alpha;
-#pragma unroll
-          for (int c = 0; c < D / 16; ++c)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              o[c][h][2 * hr] *= alpha;
-              o[c][h][2 * hr + 1] *= alpha;
-            }
+          for (int rt = 0; rt < RT; ++rt) mma_f16_16816(s[rt][j], qf[rt], b0, b1);
         }
       }
     }
-    uint32_t a[kQTile / 16][4];
-    const float mu[2] = {m_run[0] == -INFINITY ? 0.f : m_run[0], m_run[1] == -INFINITY ? 0.f : m_run[1]};
+    const bool all_seen = base + kQTile <= ce && base + kQTile - 1 <= pmin && pmax - base < p.win;
+    uint32_t a[RT][kQTile / 16][4];
 #pragma unroll
-    for (int j = 0; j < kQTile / 8; ++j) {
-      const float2 f0 = *reinterpret_cast<const float2*>(&fac[j * 8 + (lane & 3) * 2].z);
-      const float2 f1 = *reinterpret_cast<const float2*>(&fac[j * 8 + (lane & 3) * 2 + 1].z);
+    for (int rt = 0; rt < RT; ++rt) {
+      float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+      for (int j = 0; j < kQTile / 8; ++j) {
+        const uint32_t at = sFac + (j * 8 + (lane & 3) * 2) * 4;
+        const uint64_t f = lds64(at), lv = lds64(at + kQTile * 4);
+#pragma unroll
+        for (int hr = 0; hr < 2; ++hr) {
+          const float2 x = f32x2_parts(f32x2_fma(pack_f32x2(s[rt][j][2 * hr], s[rt][j][2 * hr + 1]), f, lv));
+          s[rt][j][2 * hr] = x.x;
+          s[rt][j][2 * hr + 1] = x.y;
+        }
+      }
+      if (!all_seen) {
+#pragma unroll
+        for (int hr = 0; hr < 2; ++hr) {
+          const int row = min(row0 + rt * 16 + (lane >> 2) + hr * 8, p.rows - 1);
+          const int own = intra ? T : T * p.n + p.s0 + q_row(p, grp, hk, row).s;
+#pragma unroll
+          for (int j = 0; j < kQTile / 8; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int c = base + j * 8 + (lane & 3) * 2 + e;
+              if (!(c < ce && c <= own && own - c < p.win)) s[rt][j][2 * hr + e] = -INFINITY;
+            }
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kQTile / 8; ++j)
+#pragma unroll
+        for (int hr = 0; hr < 2; ++hr) mx[hr] = fmaxf(mx[hr], fmaxf(s[rt][j][2 * hr], s[rt][j][2 * hr + 1]));
+      if (__any_sync(0xffffffffu, mx[0] > m_run[rt][0] + 15.f || mx[1] > m_run[rt][1] + 15.f)) {
+#pragma unroll
+        for (int hr = 0; hr < 2; ++hr) {
+          float m = fmaxf(mx[hr], __shfl_xor_sync(0xffffffffu, mx[hr], 1));
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+          if (m > m_run[rt][hr] + 15.f) {
+            const float alpha = fast_exp2(m_run[rt][hr] - (m - 13.f));
+            m_run[rt][hr] = m - 13.f;
+            const float2 l = f32x2_parts(l_run[rt][hr]);
+            l_run[rt][hr] = pack_f32x2(l.x * alpha, l.y * alpha);
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                o[rt][c][h][2 * hr] *= alpha;
+                o[rt][c][h][2 * hr + 1] *= alpha;
+              }
+          }
+        }
+      }
 #pragma unroll
       for (int hr = 0; hr < 2; ++hr) {
-        const float w0 = fast_exp2(s[j][2 * hr] - mu[hr]), w1 = fast_exp2(s[j][2 * hr + 1] - mu[hr]);
-        l_run[hr] = fmaf(w0, f0.x, l_run[hr]);
-        l_run[hr] = fmaf(w1, f1.x, l_run[hr]);
-        a[j / 2][2 * (j & 1) + hr] = pack_half(w0 * f0.y, w1 * f1.y);
+        const float mu = m_run[rt][hr] == -INFINITY ? 0.f : -m_run[rt][hr];
+        const uint64_t mu2 = pack_f32x2(mu, mu);
+#pragma unroll
+        for (int j = 0; j < kQTile / 8; ++j) {
+          const uint64_t iv = lds64(sFac + (2 * kQTile + j * 8 + (lane & 3) * 2) * 4);
+          const float2 x = f32x2_parts(f32x2_add(pack_f32x2(s[rt][j][2 * hr], s[rt][j][2 * hr + 1]), mu2));
+          const float w0 = fast_exp2(x.x), w1 = fast_exp2(x.y);
+          l_run[rt][hr] = f32x2_fma(pack_f32x2(w0, w1), iv, l_run[rt][hr]);
+          a[rt][j / 2][2 * (j & 1) + hr] = pack_half(w0, w1);
+        }
       }
     }
 #pragma unroll
@@ -369,46 +430,52 @@ __global__ void __launch_bounds__(kQThreads, 2)
           uint32_t e0, o0, e1, o1;
           to_half<FMT, false>(r[2 * i], e0, o0);
           to_half<FMT, false>(r[2 * i + 1], e1, o1);
-          mma_f16_16816(o[c + i][0], a[k16], e0, e1);
-          mma_f16_16816(o[c + i][1], a[k16], o0, o1);
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt) {
+            mma_f16_16816(o[rt][c + i][0], a[rt][k16], e0, e1);
+            mma_f16_16816(o[rt][c + i][1], a[rt][k16], o0, o1);
+          }
         }
       }
-    __syncwarp();  // every lane has read the tile before the next one replaces it
+    __syncwarp();  // every lane has read the tile and its scales before the next ones replace them
     if (lane == 0 && done + S < tiles) load(done + S);
   }
   // (only after a wait gave up) copies in flight end before the CTA does
   for (int i = done; i < tiles && i < done + S; ++i)
     for (const long long t0 = clock64(); !tc::mbar_try_wait(bars + (i % S) * 8, (i / S) & 1);)
       if (clock64() - t0 > (1LL << 28)) break;
+  if (p.splits > 1) asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   __syncthreads();
 
-  // ---- merge the warps' states in shared memory: per warp [16][D+4] floats
+  // ---- merge the warps' states in shared memory: per warp [ROWS][D+4] floats
   float* mbuf = reinterpret_cast<float*>(smem);
   constexpr int RS = D + 4;
 #pragma unroll
-  for (int hr = 0; hr < 2; ++hr) {
-    float l = l_run[hr];
-    l += __shfl_xor_sync(0xffffffffu, l, 1);
-    l += __shfl_xor_sync(0xffffffffu, l, 2);
-    float* rowp = mbuf + (warp * 16 + (lane >> 2) + hr * 8) * RS;
-    if ((lane & 3) == 0) {
-      rowp[D] = m_run[hr];
-      rowp[D + 1] = l;
-    }
+  for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-    for (int c = 0; c < D / 16; ++c)
-      *reinterpret_cast<float4*>(rowp + c * 16 + (lane & 3) * 4) =
-          make_float4(o[c][0][2 * hr], o[c][1][2 * hr], o[c][0][2 * hr + 1], o[c][1][2 * hr + 1]);
-  }
+    for (int hr = 0; hr < 2; ++hr) {
+      const float2 lp = f32x2_parts(l_run[rt][hr]);
+      float l = lp.x + lp.y;
+      l += __shfl_xor_sync(0xffffffffu, l, 1);
+      l += __shfl_xor_sync(0xffffffffu, l, 2);
+      float* rowp = mbuf + (warp * ROWS + rt * 16 + (lane >> 2) + hr * 8) * RS;
+      if ((lane & 3) == 0) {
+        rowp[D] = m_run[rt][hr];
+        rowp[D + 1] = l;
+      }
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c)
+        *reinterpret_cast<float4*>(rowp + c * 16 + (lane & 3) * 4) =
+            make_float4(o[rt][c][0][2 * hr], o[rt][c][1][2 * hr], o[rt][c][0][2 * hr + 1], o[rt][c][1][2 * hr + 1]);
+    }
   __syncthreads();
   if (*abort_flag) return;
-  for (int i = tid; i < 16 * D / 4; i += kQThreads) {
+  for (int i = tid; i < valid_rows * (D / 4); i += kQThreads) {
     const int lr = i / (D / 4), col4 = (i % (D / 4)) * 4;
-    if (mt * 16 + lr >= p.rows) continue;
     float mw[kQWarps], m = -INFINITY;
 #pragma unroll
     for (int w = 0; w < kQWarps; ++w) {
-      mw[w] = mbuf[(w * 16 + lr) * RS + D];
+      mw[w] = mbuf[(w * ROWS + lr) * RS + D];
       m = fmaxf(m, mw[w]);
     }
     const float mref = (m == -INFINITY) ? 0.f : m;
@@ -417,20 +484,20 @@ __global__ void __launch_bounds__(kQThreads, 2)
 #pragma unroll
     for (int w = 0; w < kQWarps; ++w) {
       const float f = fast_exp2(mw[w] - mref);
-      const float4 x = *reinterpret_cast<const float4*>(mbuf + (w * 16 + lr) * RS + col4);
+      const float4 x = *reinterpret_cast<const float4*>(mbuf + (w * ROWS + lr) * RS + col4);
       acc.x += f * x.x;
       acc.y += f * x.y;
       acc.z += f * x.z;
       acc.w += f * x.w;
-      lt += f * mbuf[(w * 16 + lr) * RS + D + 1];
+      lt += f * mbuf[(w * ROWS + lr) * RS + D + 1];
     }
     if (p.splits > 1) {
       const long long pi = (part_row0 + lr) * p.splits + split;
       if (!in_bounds(pi, 1, p.ext_part, p.status)) continue;
       *reinterpret_cast<float4*>(p.part_o + pi * D + col4) = acc;
-      if (col4 == 0) *reinterpret_cast<float2*>(p.part_ml + pi * 2) = make_float2(m, lt);
+      if (col4 == 0) reinterpret_cast<float2*>(p.part_ml)[pi] = make_float2(m, lt);
     } else {
-      const QRow r = q_row(p, grp, hk, mt * 16 + lr);
+      const QRow r = q_row(p, grp, hk, row0 + lr);
       const long long oi = ((static_cast<long long>(b) * p.nq + r.s) * p.Hq + r.h) * D;
       const long long li = (static_cast<long long>(b) * p.Hq + r.h) * p.nq + r.s;
       if (!in_bounds(oi, D, p.ext_q, p.status) || !in_bounds(li, 1, p.ext_lse, p.status)) continue;
@@ -442,52 +509,75 @@ __global__ void __launch_bounds__(kQThreads, 2)
   }
 }
 
-// One warp a query row: the chunks' partials joined.
+// The chunks' partials of a query row joined, one CTA a row: its groups of D / 4
+// threads take the chunks in turn. Launched while the first kernel's last CTAs
+// still run; what they wrote is there once griddepcontrol.wait returns.
 template <int D>
-__global__ void decode_q8_combine_kernel(const DecodeQ8Params p) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long gi = static_cast<long long>(blockIdx.x) * (blockDim.x >> 5) + warp;
-  const long long problems = static_cast<long long>(p.B) * p.Hkv * p.groups;
-  if (gi >= problems * p.rows) return;
-  const int row = static_cast<int>(gi % p.rows);
-  const long long prob = gi / p.rows;
-  const int grp = static_cast<int>(prob % p.groups);
-  const int hk = static_cast<int>((prob / p.groups) % p.Hkv);
-  const int b = static_cast<int>(prob / (static_cast<long long>(p.groups) * p.Hkv));
-  const QRow r = q_row(p, grp, hk, row);
-  const long long prow = prob * p.mt * 16 + row;
+__global__ void __launch_bounds__(kQThreads) decode_q8_combine_kernel(const DecodeQ8Params p) {
+  constexpr int LPR = D / 4, G = kQThreads / LPR;
+  __shared__ float red[2][kQWarps];
+  __shared__ float4 sum[G][LPR];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t prob = p.div_rows.div(blockIdx.x);
+  const int row = static_cast<int>(blockIdx.x - prob * p.rows);
+  const uint32_t bh = p.div_groups.div(prob);
+  const int b = static_cast<int>(p.div_hkv.div(bh));
+  const QRow r = q_row(p, static_cast<int>(prob - bh * p.groups), static_cast<int>(bh) - b * p.Hkv, row);
+  const long long first = (static_cast<long long>(prob) * p.mt * p.tile_rows + row) * p.splits;
   const long long oi = ((static_cast<long long>(b) * p.nq + r.s) * p.Hq + r.h) * D;
   const long long li = (static_cast<long long>(b) * p.Hq + r.h) * p.nq + r.s;
-  if (!in_bounds(prow * p.splits, p.splits, p.ext_part, p.status) || !in_bounds(oi, D, p.ext_q, p.status) ||
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  if (!in_bounds(first, p.splits, p.ext_part, p.status) || !in_bounds(oi, D, p.ext_q, p.status) ||
       !in_bounds(li, 1, p.ext_lse, p.status))
     return;
-
+  const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + first;
   float mx = -INFINITY;
-  for (int j = lane; j < p.splits; j += 32) mx = fmaxf(mx, p.part_ml[(prow * p.splits + j) * 2]);
+  for (int j = tid; j < p.splits; j += kQThreads) mx = fmaxf(mx, ml[j].x);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  if (lane == 0) red[0][warp] = mx;
+  __syncthreads();
+  mx = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
   const float mu = (mx == -INFINITY) ? 0.f : mx;
-  constexpr int PER = D / 32;
-  float acc[PER];
-#pragma unroll
-  for (int i = 0; i < PER; ++i) acc[i] = 0.f;
   float lt = 0.f;
-  for (int j = 0; j < p.splits; ++j) {
-    const float* ml = p.part_ml + (prow * p.splits + j) * 2;
+  for (int j = tid; j < p.splits; j += kQThreads) {
+    const float2 x = ml[j];
+    if (x.y != 0.f) lt += fast_exp2(x.x - mu) * x.y;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) lt += __shfl_xor_sync(0xffffffffu, lt, o);
+  if (lane == 0) red[1][warp] = lt;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int j = tid / LPR; j < p.splits; j += G) {
+    const float2 x = ml[j];
     // a chunk without a visible key has sum 0, and its partial O may never have
     // been written; a sum that is no number is carried on
-    if (ml[1] == 0.f) continue;
-    const float f = fast_exp2(ml[0] - mu);
-    lt += f * ml[1];
-    const float* po = p.part_o + (prow * p.splits + j) * D;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) acc[i] += f * po[lane + 32 * i];
+    if (x.y == 0.f) continue;
+    const float f = fast_exp2(x.x - mu);
+    const float4 v = *reinterpret_cast<const float4*>(p.part_o + (first + j) * D + (tid % LPR) * 4);
+    acc.x += f * v.x;
+    acc.y += f * v.y;
+    acc.z += f * v.z;
+    acc.w += f * v.w;
   }
-  const float inv = lt == 0.f ? 0.f : 1.f / lt;
-  __nv_bfloat16* out = p.o + oi;
+  sum[tid / LPR][tid % LPR] = acc;
+  __syncthreads();
+  lt = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
+  if (tid < LPR) {
 #pragma unroll
-  for (int i = 0; i < PER; ++i) out[lane + 32 * i] = __float2bfloat16_rn(acc[i] * inv);
-  if (lane == 0) p.lse[li] = lt == 0.f ? -INFINITY : (mx + __log2f(lt)) * kLn2;
+    for (int i = 1; i < G; ++i) {
+      const float4 v = sum[i][tid];
+      acc.x += v.x;
+      acc.y += v.y;
+      acc.z += v.z;
+      acc.w += v.w;
+    }
+    const float inv = lt == 0.f ? 0.f : 1.f / lt;
+    *reinterpret_cast<uint2*>(p.o + oi + tid * 4) =
+        make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+    if (tid == 0) p.lse[li] = lt == 0.f ? -INFINITY : (mx + __log2f(lt)) * kLn2;
+  }
 }
 
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
@@ -523,53 +613,88 @@ bool make_map(CUtensorMap* map, const uint8_t* base, long long J, long long R, l
             CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, int FMT>
+template <int D, int FMT, int RT>
 cudaError_t launch_decode_q8_d(const DecodeQ8Params& p, cudaStream_t stream) {
   const bool intra = p.kpt == 1 && p.n > 1;
   const long long J = intra ? static_cast<long long>(p.n) * p.Hkv : p.Hkv;
   const long long R = intra ? p.Tcap : static_cast<long long>(p.Tcap) * p.n;
   CUtensorMap mk, mv;
   if (!make_map<D>(&mk, p.kc, J, R, p.B) || !make_map<D>(&mv, p.vc, J, R, p.B)) return cudaErrorInvalidValue;
-  const int smem = Q8Smem<D>::TOTAL;
-  cudaError_t e = cudaFuncSetAttribute(decode_q8_split_kernel<D, FMT>,
+  const int smem = Q8Smem<D, RT>::TOTAL;
+  cudaError_t e = cudaFuncSetAttribute(decode_q8_split_kernel<D, FMT, RT>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  const long long blocks = static_cast<long long>(p.B) * p.Hkv * p.groups * p.splits * p.mt;
-  decode_q8_split_kernel<D, FMT><<<static_cast<unsigned>(blocks), kQThreads, smem, stream>>>(p, mk, mv);
+  const long long problems = static_cast<long long>(p.B) * p.Hkv * p.groups;
+  decode_q8_split_kernel<D, FMT, RT>
+      <<<static_cast<unsigned>(problems * p.splits * p.mt), kQThreads, smem, stream>>>(p, mk, mv);
   e = cudaGetLastError();
   if (e != cudaSuccess || p.splits == 1) return e;
-  const long long rows = static_cast<long long>(p.B) * p.Hkv * p.groups * p.rows;
-  decode_q8_combine_kernel<D><<<static_cast<unsigned>((rows + 7) / 8), 256, 0, stream>>>(p);
-  return cudaGetLastError();
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(problems * p.rows));
+  cfg.blockDim = dim3(kQThreads);
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, decode_q8_combine_kernel<D>, p);
+}
+
+template <int D, int FMT>
+cudaError_t launch_decode_q8_rt(const DecodeQ8Params& p, cudaStream_t stream) {
+  if (p.tile_rows == 16) return launch_decode_q8_d<D, FMT, 1>(p, stream);
+  if (p.tile_rows == 32) return launch_decode_q8_d<D, FMT, 2>(p, stream);
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace
 
-// Chunks of whole rounds of the warps (128 keys), four waves of two CTAs an SM
-// where the cache is long enough for chunks of 512 keys and more.
-long long decode_q8_most_splits(long long problems, long long keys, int sms) {
-  const long long round = kQWarps * kQTile;
-  const long long target = static_cast<long long>(sms) * 2 * 4;
-  const long long sp = (target + problems - 1) / problems;
-  const long long most = (keys + 4 * round - 1) / (4 * round);
-  return sp < most ? sp : most;
+// Rows of a CTA.
+int decode_q8_tile_rows(int rows) { return rows <= 16 ? 16 : 32; }
+
+constexpr int kMaxWaves = 16;
+
+int q8_ctas_per_sm(int tile_rows) { return tile_rows == 16 ? Q8Smem<128, 1>::CTAS : Q8Smem<128, 2>::CTAS; }
+
+long long decode_q8_most_splits(long long problems, long long keys, int tile_rows, int sms) {
+  const long long rounds = (keys + kQ8Round - 1) / kQ8Round;
+  const long long fit = static_cast<long long>(sms) * q8_ctas_per_sm(tile_rows) * kMaxWaves / problems;
+  return fit < 1 ? 1 : (fit < rounds ? fit : rounds);
 }
 
-void decode_q8_plan(long long problems, long long keys, int sms, int* splits, int* chunk) {
-  const long long round = kQWarps * kQTile;
-  const long long sp = decode_q8_most_splits(problems, keys, sms);
-  long long ch = (keys + sp - 1) / sp;
-  ch = (ch + round - 1) / round * round;
-  *splits = static_cast<int>((keys + ch - 1) / ch);
-  *chunk = static_cast<int>(ch);
+// Chunks of whole rounds of the warps (128 keys). A CTA's time is its rounds and
+// about kOverhead more (its start, its merge and its share of the join). For each
+// number of waves the chunks that just fill it are tried, and those that need
+// the least time in all are taken.
+void decode_q8_plan(long long problems, long long keys, int tile_rows, int sms, int* splits, int* chunk) {
+  constexpr long long kOverhead = 4;
+  const long long rounds = (keys + kQ8Round - 1) / kQ8Round;
+  const long long slots = static_cast<long long>(sms) * q8_ctas_per_sm(tile_rows);
+  const long long most = decode_q8_most_splits(problems, keys, tile_rows, sms);
+  long long per = rounds, least = ((problems + slots - 1) / slots) * (rounds + kOverhead / 2);
+  for (int w = 1; w <= kMaxWaves; ++w) {
+    long long n = slots * w / problems;
+    if (n > most) n = most;
+    if (n < 2) continue;
+    const long long r = (rounds + n - 1) / n;
+    const long long time = ((problems * ((rounds + r - 1) / r) + slots - 1) / slots) * (r + kOverhead);
+    if (time < least) {
+      least = time;
+      per = r;
+    }
+    if (n == most) break;
+  }
+  *splits = static_cast<int>((rounds + per - 1) / per);
+  *chunk = static_cast<int>(per * kQ8Round);
 }
 
 cudaError_t launch_decode_q8(const DecodeQ8Params& p, cudaStream_t stream) {
   const bool e4m3 = p.format == HD_Q8_E4M3;
   if (p.D == 64)
-    return e4m3 ? launch_decode_q8_d<64, HD_Q8_E4M3>(p, stream) : launch_decode_q8_d<64, HD_Q8_INT8>(p, stream);
+    return e4m3 ? launch_decode_q8_rt<64, HD_Q8_E4M3>(p, stream) : launch_decode_q8_rt<64, HD_Q8_INT8>(p, stream);
   if (p.D == 128)
-    return e4m3 ? launch_decode_q8_d<128, HD_Q8_E4M3>(p, stream) : launch_decode_q8_d<128, HD_Q8_INT8>(p, stream);
+    return e4m3 ? launch_decode_q8_rt<128, HD_Q8_E4M3>(p, stream) : launch_decode_q8_rt<128, HD_Q8_INT8>(p, stream);
   return cudaErrorInvalidValue;
 }
 
