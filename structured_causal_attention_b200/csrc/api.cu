@@ -266,9 +266,10 @@ int kv_q8_params(KvQ8Params& p, const int32_t* token_offset, const int32_t* leng
   return HD_OK;
 }
 
-// Problems, keys and splits of a decode step over the 8-bit cache: sets nq, s0,
-// groups, spg, kpt, win, rows, mt, splits and chunk from the sizes.
-void decode_q8_problem(DecodeQ8Params& p, int mode, int W_tokens, int final_only) {
+// Problems and pieces of a decode step over the 8-bit cache: sets nq, s0, groups,
+// spg, kpt, win, g, rows, tile_rows, mt, ctas, least, whole and slots from the
+// sizes. Returns the bytes of its workspace.
+size_t decode_q8_problem(DecodeQ8Params& p, int mode, int W_tokens, int final_only) {
   p.nq = final_only ? 1 : p.n;
   p.s0 = final_only ? p.n - 1 : 0;
   p.groups = mode == HD_INTRA ? p.nq : 1;
@@ -286,11 +287,17 @@ void decode_q8_problem(DecodeQ8Params& p, int mode, int W_tokens, int final_only
   p.rows = p.spg * p.g;
   p.tile_rows = decode_q8_tile_rows(p.rows);
   p.mt = (p.rows + p.tile_rows - 1) / p.tile_rows;
-  decode_q8_plan(static_cast<long long>(p.B) * p.Hkv * p.groups * p.mt, keys, p.tile_rows, sm_count(), &p.splits,
-                 &p.chunk);
+  const long long problems = static_cast<long long>(p.B) * p.groups;
+  decode_q8_plan(problems, keys, p.tile_rows, static_cast<long long>(p.Hkv) * p.mt, sm_count(), &p.ctas, &p.least,
+                 &p.whole);
+  p.slots = static_cast<int>(problems) + p.ctas;
+  const size_t prow = p.whole ? 1 : static_cast<size_t>(p.mt) * p.Hkv * p.tile_rows * p.slots;  // (never empty)
+  p.ext_part = static_cast<long long>(prow);
+  return align256(prow * static_cast<size_t>(p.D) * 4) + align256(prow * 2 * 4);
 }
 
-// The most that any mode needs of one decode step over the 8-bit cache.
+// The most that any mode and window needs. (A window's pieces are no more than
+// those of the whole cache.)
 size_t decode_q8_workspace(int B, int n, int Tcap, int Hq, int Hkv, int D, int final_only) {
   if (B < 1 || n < 1 || Tcap < 1 || Hq < 1 || Hkv < 1 || D < 1 || Hq % Hkv) return 0;
   size_t most = 0;
@@ -301,12 +308,8 @@ size_t decode_q8_workspace(int B, int n, int Tcap, int Hq, int Hkv, int D, int f
     p.Tcap = Tcap;
     p.Hq = Hq;
     p.Hkv = Hkv;
-    decode_q8_problem(p, mode, 1, final_only);
-    const long long problems = static_cast<long long>(B) * Hkv * p.groups * p.mt;
-    const long long splits = decode_q8_most_splits(problems, static_cast<long long>(Tcap) * p.kpt, p.tile_rows,
-                                                   sm_count());
-    const size_t prow = static_cast<size_t>(problems) * p.tile_rows * static_cast<size_t>(splits);
-    const size_t need = align256(prow * static_cast<size_t>(D) * 4) + align256(prow * 2 * 4);
+    p.D = D;
+    const size_t need = decode_q8_problem(p, mode, 1, final_only);
     if (need > most) most = need;
   }
   return most;
@@ -329,6 +332,10 @@ int decode_q8_call(const void* q, const void* k_codes, const void* v_codes, cons
       !aligned16(v_scale) || !aligned16(out) || !aligned16(workspace))
     return HD_ERR_INVALID_ARG;
   if (static_cast<long long>(Tcap) * n * Hkv * D >= 1LL << 40) return HD_ERR_UNSUPPORTED;  // a TMA stride
+  // rows of the output and rounds of the line are counted in 32 bits
+  const long long per_token = static_cast<long long>(B) * n * Hq;
+  if (per_token > 1LL << 30 || per_token * ((static_cast<long long>(Tcap) * n + kQ8Round - 1) / kQ8Round) > 1LL << 30)
+    return HD_ERR_UNSUPPORTED;
   if (workspace_bytes < decode_q8_workspace(B, n, Tcap, Hq, Hkv, D, final_only)) return HD_ERR_INVALID_ARG;
   DecodeQ8Params p = {};
   p.q = static_cast<const __nv_bfloat16*>(q);
@@ -351,8 +358,6 @@ int decode_q8_call(const void* q, const void* k_codes, const void* v_codes, cons
   p.nb = q8_blocks(Tcap, block_tokens);
   p.scale_log2 = scale * 1.4426950408889634074f;
   decode_q8_problem(p, mode, W_tokens, final_only);
-  if (static_cast<long long>(B) * Hkv * p.groups * p.mt * p.splits * p.tile_rows > (1LL << 31) - 1) return HD_ERR_UNSUPPORTED;
-  const size_t prow = static_cast<size_t>(B) * Hkv * p.groups * p.mt * p.tile_rows * p.splits;
   const bool intra = p.kpt == 1 && n > 1;
   const int step_tok = intra ? kQ8Round : kQ8Round / n;
   p.step_stream = intra ? 0 : kQ8Round % n;
@@ -360,7 +365,6 @@ int decode_q8_call(const void* q, const void* k_codes, const void* v_codes, cons
   p.step_off = step_tok % p.bt;
   p.div_g = FastDiv::by(p.g);
   p.div_mt = FastDiv::by(p.mt);
-  p.div_splits = FastDiv::by(p.splits);
   p.div_groups = FastDiv::by(p.groups);
   p.div_hkv = FastDiv::by(Hkv);
   p.div_rows = FastDiv::by(p.rows);
@@ -369,9 +373,9 @@ int decode_q8_call(const void* q, const void* k_codes, const void* v_codes, cons
   p.ext_q = static_cast<long long>(B) * p.nq * Hq * D;
   p.ext_lse = static_cast<long long>(B) * Hq * p.nq;
   p.ext_scale = static_cast<long long>(B) * Hkv * p.nb * n;
-  p.ext_part = static_cast<long long>(prow);
   p.part_o = static_cast<float*>(workspace);
-  p.part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + align256(prow * D * 4));
+  p.part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) +
+                                       align256(static_cast<size_t>(p.ext_part) * D * 4));
   return from_cuda(launch_decode_q8(p, static_cast<cudaStream_t>(stream)));
 }
 

@@ -22,11 +22,20 @@
 //
 // Under INTRA each stream is a problem of its own (g query rows, every n-th
 // position), so every loaded key is visible and none is read twice; otherwise
-// the n*g rows of a KV head share the keys. A CTA owns (sequence, KV head, stream
-// group, tile of 16 RT rows, chunk of keys); its warps each stream 32-key tiles
-// of their own through a TMA ring of their own, with nothing between warps until
-// their states are merged at the end. The kernel writes the output itself where
-// one chunk holds the whole cache, else partials that a second kernel joins.
+// the n*g rows of a KV head share the keys.
+//
+// The work is one line of rounds of 128 keys for each KV head: all rounds of the
+// first problem (sequence, stream group), then of the next, as the lengths on the
+// device have it. As many CTAs as fit the GPU at once each take an equal piece of
+// a head's line, whatever the lengths, so a ragged batch keeps every SM busy. The
+// heads' CTAs walk their lines side by side, as neighbouring heads lie side by
+// side in a row of the cache: with one line through all heads in turn, whose
+// rows are then fetched in scattered pieces of 128 (64) bytes, a step at D = 128
+// took 10% longer and at D = 64 30%. Within a
+// problem a CTA's warps each stream 32-key tiles of their own through a TMA ring
+// of their own, with nothing between warps until their states are merged. A
+// problem that one CTA has whole is written by it; of the others each piece goes
+// to the workspace, and a second kernel joins them.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -117,6 +126,13 @@ __device__ __forceinline__ float2 f32x2_parts(uint64_t a) {
   asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(a));
   return f;
 }
+// A load that stays where it is written: the compiler moved a plain one down to
+// its use in the next step, whose wait for it took a fifth of the time.
+__device__ __forceinline__ float ldg_here(const float* at) {
+  float x;
+  asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(x) : "l"(at));
+  return x;
+}
 __device__ __forceinline__ uint64_t lds64(uint32_t addr) {
   uint64_t r;
   asm volatile("ld.shared.b64 %0, [%1];" : "=l"(r) : "r"(addr));
@@ -132,6 +148,78 @@ __device__ __forceinline__ QRow q_row(const DecodeQ8Params& p, int grp, int hk, 
   return {grp * p.spg + sg, hk * p.g + row - sg * p.g};
 }
 
+// Row `row` of group grp of sequence b and KV head hk, among the rows of q and
+// out, and its place in lse.
+__device__ __forceinline__ long long out_row(const DecodeQ8Params& p, int b, int grp, int hk, int row) {
+  const QRow r = q_row(p, grp, hk, row);
+  return (static_cast<long long>(b) * p.nq + r.s) * p.Hq + r.h;
+}
+__device__ __forceinline__ long long lse_at(const DecodeQ8Params& p, int b, int grp, int hk, int row) {
+  const QRow r = q_row(p, grp, hk, row);
+  return (static_cast<long long>(b) * p.Hq + r.h) * p.nq + r.s;
+}
+// A sequence whose length is out of range: a row of zeros.
+template <int D>
+__device__ __forceinline__ void zero_row(const DecodeQ8Params& p, int b, int grp, int hk, int row) {
+  const long long o = out_row(p, b, grp, hk, row) * D, li = lse_at(p, b, grp, hk, row);
+  if (!in_bounds(o, D, p.ext_q, p.status) || !in_bounds(li, 1, p.ext_lse, p.status)) return;
+  for (int i = 0; i < D; i += 8) *reinterpret_cast<uint4*>(p.o + o + i) = make_uint4(0, 0, 0, 0);
+  p.lse[li] = -INFINITY;
+}
+// Row lr of the row tile at row0 of head hk in the workspace, of the part that a
+// CTA has of a problem. Its slot is the problem's number plus the CTA's: along the
+// line one or the other grows from part to part, so no two share a slot.
+__device__ __forceinline__ long long part_row(const DecodeQ8Params& p, int hk, int row0, int slot, int lr) {
+  return (static_cast<long long>(row0) * p.Hkv + static_cast<long long>(hk) * p.tile_rows) * p.slots +
+         static_cast<long long>(slot) * p.tile_rows + lr;
+}
+
+// Rounds of 128 keys that a problem of sequence b has: 0 where its length is out
+// of range.
+__device__ __forceinline__ int q8_rounds(const DecodeQ8Params& p, int b) {
+  const int T1 = __ldg(p.seqlen + b);
+  if (T1 < 1 || T1 > p.Tcap) return 0;
+  const int first = p.kpt == 1 && p.n > 1 ? T1 - 1 : (T1 - 1) * p.n + p.s0;  // the first query's own key
+  return (T1 * p.kpt - max(0, first - p.win + 1) + kQ8Round - 1) / kQ8Round;
+}
+
+// The line of all problems' rounds (of one KV head), and the CTAs' pieces of it.
+struct Q8Line {
+  int total, piece;
+  // Rounds before sequence b.
+  __device__ __forceinline__ int before(const DecodeQ8Params& p, int lane, int b) const {
+    int sum = 0;
+    for (int i = lane; i < b; i += 32) sum += q8_rounds(p, i);
+    return __reduce_add_sync(0xffffffffu, sum) * p.groups;
+  }
+  // The sequence that has round pos < total, and pos within its rounds.
+  __device__ __forceinline__ int sequence(const DecodeQ8Params& p, int lane, int pos, int& within) const {
+    int start = 0;
+    for (int i0 = 0;; i0 += 32) {
+      const int mine = i0 + lane < p.B ? q8_rounds(p, i0 + lane) * p.groups : 0;
+      int sum = mine;  // of the lanes up to this one
+#pragma unroll
+      for (int d = 1; d < 32; d *= 2) {
+        const int x = __shfl_up_sync(0xffffffffu, sum, d);
+        if (lane >= d) sum += x;
+      }
+      const uint32_t past = __ballot_sync(0xffffffffu, start + sum > pos);
+      if (past != 0) {
+        const int l = __ffs(past) - 1;
+        within = pos - start - __shfl_sync(0xffffffffu, sum - mine, l);
+        return i0 + l;
+      }
+      start += __shfl_sync(0xffffffffu, sum, 31);
+    }
+  }
+};
+__device__ __forceinline__ Q8Line q8_line(const DecodeQ8Params& p, int lane) {
+  int sum = 0;
+  for (int i = lane; i < p.B; i += 32) sum += q8_rounds(p, i);
+  const int total = __reduce_add_sync(0xffffffffu, sum) * p.groups;
+  return {total, max((total + p.ctas - 1) / p.ctas, p.least)};
+}
+
 template <int D, int FMT, int RT>
 __global__ void __launch_bounds__(kQThreads, Q8Smem<D, RT>::CTAS)
     decode_q8_split_kernel(const DecodeQ8Params p, const __grid_constant__ CUtensorMap tmK,
@@ -145,69 +233,68 @@ __global__ void __launch_bounds__(kQThreads, Q8Smem<D, RT>::CTAS)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int* after = reinterpret_cast<int*>(smem + SM::RING + SM::Q + SM::FAC + SM::BARS);
   volatile int* abort_flag = after;
-  uint32_t idx = blockIdx.x, rest = p.div_mt.div(idx);
-  const int mt = static_cast<int>(idx - rest * p.mt);
-  idx = rest;
-  rest = p.div_splits.div(idx);
-  const int split = static_cast<int>(idx - rest * p.splits);
-  const uint32_t prob = rest;  // (sequence, KV head, group)
-  rest = p.div_groups.div(prob);
-  const int grp = static_cast<int>(prob - rest * p.groups);
-  const int b = static_cast<int>(p.div_hkv.div(rest));
-  const int hk = static_cast<int>(rest) - b * p.Hkv;
-
-  const int T1 = __ldg(p.seqlen + b);
-  const bool ok = T1 >= 1 && T1 <= p.Tcap;
-  if (!ok && tid == 0 && mt == 0 && split == 0 && grp == 0 && hk == 0) record_status(p.status, HD_ERR_DEVICE_INDEX);
-  const int T = ok ? T1 - 1 : 0;
+  const uint32_t bars = sQ + SM::Q + SM::FAC + warp * S * 8;
+  const uint32_t ring = sRing + warp * S * 2 * SM::KV;
+  if (lane == 0) {
+    for (int i = 0; i < S; ++i) tc::mbar_init(bars + i * 8, 1);
+    tc::fence_mbar_init();
+    tc::fence_async_smem();
+  }
+  if (tid == 0) *abort_flag = 0;
+  if (!p.whole) asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  const uint32_t line_head = p.div_mt.div(blockIdx.x);  // row tiles, then heads, side by side
+  const int row0 = static_cast<int>(blockIdx.x - line_head * p.mt) * ROWS, valid_rows = min(ROWS, p.rows - row0);
+  const int cta = static_cast<int>(p.div_hkv.div(line_head)), hk = static_cast<int>(line_head) - cta * p.Hkv;
   const bool intra = p.kpt == 1 && p.n > 1;       // keys are the tokens of one stream
-  const int kend = ok ? T1 * p.kpt : 0;
+
+  // ---- this CTA's piece: rounds pos .. end-1 of the line; of sequence b, group grp
+  // of it, r0 of its `rounds`
+  int pos, end, b, grp, r0, rounds;
+  if (p.whole) {  // (a problem a CTA)
+    b = static_cast<int>(p.div_groups.div(cta));
+    grp = cta - b * p.groups;
+    rounds = q8_rounds(p, b);
+    if (rounds == 0) {
+      if (grp == 0 && hk == 0 && tid == 0 && row0 == 0) record_status(p.status, HD_ERR_DEVICE_INDEX);
+      if (tid < valid_rows) zero_row<D>(p, b, grp, hk, row0 + tid);
+      return;
+    }
+    pos = r0 = 0;
+    end = rounds;
+  } else {
+    const Q8Line line = q8_line(p, lane);
+    pos = cta * line.piece;
+    end = min(pos + line.piece, line.total);
+    if (pos >= end) return;
+    b = line.sequence(p, lane, pos, r0);  // r0: rounds of the sequence before pos
+    rounds = q8_rounds(p, b);
+    grp = r0 / rounds;
+    r0 -= grp * rounds;
+  }
+
+  int it = 0;  // tiles of this warp so far: a tile's stage and the parity of its barrier
+  while (true) {
+  const int r1 = min(rounds, r0 + end - pos);
+  const int T = __ldg(p.seqlen + b) - 1;
   const int pmin = intra ? T : T * p.n + p.s0;    // the first and last query's own key
   const int pmax = intra ? T : T * p.n + p.s0 + p.nq - 1;
   const int kbeg = max(0, pmin - p.win + 1);      // (win is beyond any cache where there is none)
-  const int cs = kbeg + split * p.chunk;
-  const int ce = min(kend, cs + p.chunk);
-  const int row0 = mt * ROWS, valid_rows = min(ROWS, p.rows - row0);
-  const long long part_row0 = static_cast<long long>(prob) * p.mt * ROWS + row0;
-
-  if (cs >= ce) {  // nothing to read in this chunk
-    if (tid < valid_rows) {
-      if (p.splits > 1) {
-        if (in_bounds((part_row0 + tid) * p.splits + split, 1, p.ext_part, p.status))
-          reinterpret_cast<float2*>(p.part_ml)[(part_row0 + tid) * p.splits + split] = make_float2(-INFINITY, 0.f);
-      } else {  // no sequence at all: a row of zeros
-        const QRow r = q_row(p, grp, hk, row0 + tid);
-        const long long oi = ((static_cast<long long>(b) * p.nq + r.s) * p.Hq + r.h) * D;
-        const long long li = (static_cast<long long>(b) * p.Hq + r.h) * p.nq + r.s;
-        if (in_bounds(oi, D, p.ext_q, p.status) && in_bounds(li, 1, p.ext_lse, p.status)) {
-          for (int i = 0; i < D; i += 8) *reinterpret_cast<uint4*>(p.o + oi + i) = make_uint4(0, 0, 0, 0);
-          p.lse[li] = -INFINITY;
-        }
-      }
-    }
-    return;
-  }
+  const int cs = kbeg + r0 * kQ8Round;
+  const int ce = min((T + 1) * p.kpt, kbeg + r1 * kQ8Round);
 
   // ---- this warp's tiles: warp, warp + 4, ... of the chunk
   const int all_tiles = (ce - cs + kQTile - 1) / kQTile;
   const int tiles = (all_tiles - warp + kQWarps - 1) / kQWarps;
-  const uint32_t ring = sRing + warp * S * 2 * SM::KV;
-  const uint32_t bars = sQ + SM::Q + SM::FAC + warp * S * 8;
   const int col = intra ? (p.s0 + grp) * p.Hkv + hk : hk;
   auto load = [&](int i) {
-    const uint32_t bar = bars + (i % S) * 8, dst = ring + (i % S) * 2 * SM::KV;
+    const uint32_t bar = bars + ((it + i) % S) * 8, dst = ring + ((it + i) % S) * 2 * SM::KV;
     const int row = cs + (i * kQWarps + warp) * kQTile;
     tc::mbar_expect_tx(bar, 2 * SM::KV);  // rows behind the tensor are filled with zeros and counted
     tc::tma_load_4d(dst, &tmK, bar, 0, col, row, b);
     tc::tma_load_4d(dst + SM::KV, &tmV, bar, 0, col, row, b);
   };
-  if (tid == 0) *abort_flag = 0;
-  if (lane == 0) {
-    for (int i = 0; i < S; ++i) tc::mbar_init(bars + i * 8, 1);
-    tc::fence_mbar_init();
-    tc::fence_async_smem();
+  if (lane == 0)
     for (int i = 0; i < S && i < tiles; ++i) load(i);
-  }
 
   // ---- the scales: lane i has key i of the tile. Its place (block, token in the
   // block, stream) moves on by kQWarps tiles a step, without a division.
@@ -222,8 +309,8 @@ __global__ void __launch_bounds__(kQThreads, Q8Smem<D, RT>::CTAS)
     vs = 1.f;
     const long long si = sc0 + static_cast<long long>(blk) * p.n + stream;
     if (key < ce && in_bounds(si, 1, p.ext_scale, p.status)) {
-      ks = __ldg(p.ks + si);
-      vs = __ldg(p.vs + si);
+      ks = ldg_here(p.ks + si);
+      vs = ldg_here(p.vs + si);
     }
     key += kQWarps * kQTile;
     blk += p.step_blk;
@@ -299,7 +386,7 @@ __global__ void __launch_bounds__(kQThreads, Q8Smem<D, RT>::CTAS)
   float* fac = reinterpret_cast<float*>(smem + SM::RING + SM::Q) + warp * (kQTile * 3);
   int done = 0;  // tiles whose copies have arrived
   for (; done < tiles; ++done) {
-    const int st = done % S;
+    const int st = (it + done) % S;
     const int base = cs + (done * kQWarps + warp) * kQTile;
     const uint32_t kb = ring + st * 2 * SM::KV, vb = kb + SM::KV;
     {
@@ -314,7 +401,7 @@ __global__ void __launch_bounds__(kQThreads, Q8Smem<D, RT>::CTAS)
       fac[2 * kQTile + lane] = fin ? __fdividef(1.f, vs) : (e == 128 ? 1.f : __int_as_float((127 - kQ8MinExp) << 23));
     }
     fetch_scales();  // of the next tile
-    if (!tc::mbar_wait_warp(bars + st * 8, (done / S) & 1, abort_flag, p.status)) break;
+    if (!tc::mbar_wait_warp(bars + st * 8, ((it + done) / S) & 1, abort_flag, p.status)) break;
     if (base + kQTile > ce) {
       // V rows behind the chunk may hold anything, and zero times a NaN is one
       for (int i = lane; i < kQTile * D / 16; i += 32)
@@ -442,9 +529,9 @@ __global__ void __launch_bounds__(kQThreads, Q8Smem<D, RT>::CTAS)
   }
   // (only after a wait gave up) copies in flight end before the CTA does
   for (int i = done; i < tiles && i < done + S; ++i)
-    for (const long long t0 = clock64(); !tc::mbar_try_wait(bars + (i % S) * 8, (i / S) & 1);)
+    for (const long long t0 = clock64(); !tc::mbar_try_wait(bars + ((it + i) % S) * 8, ((it + i) / S) & 1);)
       if (clock64() - t0 > (1LL << 28)) break;
-  if (p.splits > 1) asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  it += tiles;
   __syncthreads();
 
   // ---- merge the warps' states in shared memory: per warp [ROWS][D+4] floats
@@ -470,6 +557,7 @@ __global__ void __launch_bounds__(kQThreads, Q8Smem<D, RT>::CTAS)
     }
   __syncthreads();
   if (*abort_flag) return;
+  const bool all = r1 - r0 == rounds;
   for (int i = tid; i < valid_rows * (D / 4); i += kQThreads) {
     const int lr = i / (D / 4), col4 = (i % (D / 4)) * 4;
     float mw[kQWarps], m = -INFINITY;
@@ -491,48 +579,68 @@ __global__ void __launch_bounds__(kQThreads, Q8Smem<D, RT>::CTAS)
       acc.w += f * x.w;
       lt += f * mbuf[(w * ROWS + lr) * RS + D + 1];
     }
-    if (p.splits > 1) {
-      const long long pi = (part_row0 + lr) * p.splits + split;
+    if (all) {
+      const long long row = out_row(p, b, grp, hk, row0 + lr), li = lse_at(p, b, grp, hk, row0 + lr);
+      if (!in_bounds(row * D, D, p.ext_q, p.status) || !in_bounds(li, 1, p.ext_lse, p.status)) continue;
+      const float inv = 1.f / lt;
+      *reinterpret_cast<uint2*>(p.o + row * D + col4) =
+          make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+      if (col4 == 0) p.lse[li] = (m + __log2f(lt)) * kLn2;
+    } else {
+      const long long pi = part_row(p, hk, row0, b * p.groups + grp + cta, lr);
       if (!in_bounds(pi, 1, p.ext_part, p.status)) continue;
       *reinterpret_cast<float4*>(p.part_o + pi * D + col4) = acc;
       if (col4 == 0) reinterpret_cast<float2*>(p.part_ml)[pi] = make_float2(m, lt);
-    } else {
-      const QRow r = q_row(p, grp, hk, row0 + lr);
-      const long long oi = ((static_cast<long long>(b) * p.nq + r.s) * p.Hq + r.h) * D;
-      const long long li = (static_cast<long long>(b) * p.Hq + r.h) * p.nq + r.s;
-      if (!in_bounds(oi, D, p.ext_q, p.status) || !in_bounds(li, 1, p.ext_lse, p.status)) continue;
-      const float inv = 1.f / lt;
-      *reinterpret_cast<uint2*>(p.o + oi + col4) =
-          make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-      if (col4 == 0) p.lse[li] = (m + __log2f(lt)) * kLn2;
     }
+  }
+  // ---- the next problem of the piece
+  pos += r1 - r0;
+  if (pos >= end) break;
+  r0 = 0;
+  if (++grp == p.groups) {
+    grp = 0;
+    do ++b;
+    while ((rounds = q8_rounds(p, b)) == 0);  // (one that is left has rounds: pos < end)
+  }
+  tc::fence_async_smem();  // the merge's writes come before the copies that replace them
+  __syncthreads();
   }
 }
 
-// The chunks' partials of a query row joined, one CTA a row: its groups of D / 4
-// threads take the chunks in turn. Launched while the first kernel's last CTAs
-// still run; what they wrote is there once griddepcontrol.wait returns.
+// The pieces of a query row joined, one CTA a row: its groups of D / 4 threads
+// take the pieces in turn. Launched while the first kernel still runs; what that
+// wrote is there once griddepcontrol.wait returns.
 template <int D>
 __global__ void __launch_bounds__(kQThreads) decode_q8_combine_kernel(const DecodeQ8Params p) {
   constexpr int LPR = D / 4, G = kQThreads / LPR;
   __shared__ float red[2][kQWarps];
   __shared__ float4 sum[G][LPR];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const uint32_t prob = p.div_rows.div(blockIdx.x);
-  const int row = static_cast<int>(blockIdx.x - prob * p.rows);
-  const uint32_t bh = p.div_groups.div(prob);
-  const int b = static_cast<int>(p.div_hkv.div(bh));
-  const QRow r = q_row(p, static_cast<int>(prob - bh * p.groups), static_cast<int>(bh) - b * p.Hkv, row);
-  const long long first = (static_cast<long long>(prob) * p.mt * p.tile_rows + row) * p.splits;
-  const long long oi = ((static_cast<long long>(b) * p.nq + r.s) * p.Hq + r.h) * D;
-  const long long li = (static_cast<long long>(b) * p.Hq + r.h) * p.nq + r.s;
+  const uint32_t unit = p.div_rows.div(blockIdx.x);
+  const int row = static_cast<int>(blockIdx.x - unit * p.rows);
+  const int prob = static_cast<int>(p.div_hkv.div(unit)), hk = static_cast<int>(unit) - prob * p.Hkv;
+  const int b = static_cast<int>(p.div_groups.div(prob)), grp = prob - b * p.groups;
+  const int rounds = q8_rounds(p, b);
+  const long long orow = out_row(p, b, grp, hk, row), li = lse_at(p, b, grp, hk, row);
+  const Q8Line line = q8_line(p, lane);
+  const int start = line.before(p, lane, b) + grp * rounds;
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
-  if (!in_bounds(first, p.splits, p.ext_part, p.status) || !in_bounds(oi, D, p.ext_q, p.status) ||
+  if (rounds == 0) {
+    if (tid == 0 && grp == 0 && hk == 0 && row == 0) record_status(p.status, HD_ERR_DEVICE_INDEX);
+    if (tid == 0) zero_row<D>(p, b, grp, hk, row);
+    return;
+  }
+  const int cta = start / line.piece, parts = (start + rounds - 1) / line.piece - cta + 1;
+  if (parts == 1) return;  // written already
+  const int row0 = row / p.tile_rows * p.tile_rows;
+  const long long first = part_row(p, hk, row0, prob + cta, row - row0);
+  const long long step = p.tile_rows;
+  if (!in_bounds(first, (parts - 1) * step + 1, p.ext_part, p.status) || !in_bounds(orow * D, D, p.ext_q, p.status) ||
       !in_bounds(li, 1, p.ext_lse, p.status))
     return;
   const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + first;
   float mx = -INFINITY;
-  for (int j = tid; j < p.splits; j += kQThreads) mx = fmaxf(mx, ml[j].x);
+  for (int j = tid; j < parts; j += kQThreads) mx = fmaxf(mx, ml[j * step].x);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
   if (lane == 0) red[0][warp] = mx;
@@ -540,22 +648,19 @@ __global__ void __launch_bounds__(kQThreads) decode_q8_combine_kernel(const Deco
   mx = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
   const float mu = (mx == -INFINITY) ? 0.f : mx;
   float lt = 0.f;
-  for (int j = tid; j < p.splits; j += kQThreads) {
-    const float2 x = ml[j];
-    if (x.y != 0.f) lt += fast_exp2(x.x - mu) * x.y;
+  for (int j = tid; j < parts; j += kQThreads) {
+    const float2 x = ml[j * step];
+    lt += fast_exp2(x.x - mu) * x.y;
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) lt += __shfl_xor_sync(0xffffffffu, lt, o);
   if (lane == 0) red[1][warp] = lt;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-  for (int j = tid / LPR; j < p.splits; j += G) {
-    const float2 x = ml[j];
-    // a chunk without a visible key has sum 0, and its partial O may never have
-    // been written; a sum that is no number is carried on
-    if (x.y == 0.f) continue;
-    const float f = fast_exp2(x.x - mu);
-    const float4 v = *reinterpret_cast<const float4*>(p.part_o + (first + j) * D + (tid % LPR) * 4);
+  for (int j = tid / LPR; j < parts; j += G) {
+    // (a piece without a key that the row sees has reference -inf and sum 0)
+    const float f = fast_exp2(ml[j * step].x - mu);
+    const float4 v = *reinterpret_cast<const float4*>(p.part_o + (first + j * step) * D + (tid % LPR) * 4);
     acc.x += f * v.x;
     acc.y += f * v.y;
     acc.z += f * v.z;
@@ -573,10 +678,10 @@ __global__ void __launch_bounds__(kQThreads) decode_q8_combine_kernel(const Deco
       acc.z += v.z;
       acc.w += v.w;
     }
-    const float inv = lt == 0.f ? 0.f : 1.f / lt;
-    *reinterpret_cast<uint2*>(p.o + oi + tid * 4) =
+    const float inv = 1.f / lt;
+    *reinterpret_cast<uint2*>(p.o + orow * D + tid * 4) =
         make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-    if (tid == 0) p.lse[li] = lt == 0.f ? -INFINITY : (mx + __log2f(lt)) * kLn2;
+    if (tid == 0) p.lse[li] = (mx + __log2f(lt)) * kLn2;
   }
 }
 
@@ -610,7 +715,7 @@ bool make_map(CUtensorMap* map, const uint8_t* base, long long J, long long R, l
   const cuuint32_t estr[4] = {1, 1, 1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<uint8_t*>(base), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int D, int FMT, int RT>
@@ -624,16 +729,14 @@ cudaError_t launch_decode_q8_d(const DecodeQ8Params& p, cudaStream_t stream) {
   cudaError_t e = cudaFuncSetAttribute(decode_q8_split_kernel<D, FMT, RT>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  const long long problems = static_cast<long long>(p.B) * p.Hkv * p.groups;
-  decode_q8_split_kernel<D, FMT, RT>
-      <<<static_cast<unsigned>(problems * p.splits * p.mt), kQThreads, smem, stream>>>(p, mk, mv);
+  decode_q8_split_kernel<D, FMT, RT><<<static_cast<unsigned>(p.ctas * p.Hkv * p.mt), kQThreads, smem, stream>>>(p, mk, mv);
   e = cudaGetLastError();
-  if (e != cudaSuccess || p.splits == 1) return e;
+  if (e != cudaSuccess || p.whole) return e;
   cudaLaunchAttribute attr = {};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(problems * p.rows));
+  cfg.gridDim = dim3(static_cast<unsigned>(p.B * p.Hkv * p.groups * p.rows));
   cfg.blockDim = dim3(kQThreads);
   cfg.stream = stream;
   cfg.attrs = &attr;
@@ -653,40 +756,17 @@ cudaError_t launch_decode_q8_rt(const DecodeQ8Params& p, cudaStream_t stream) {
 // Rows of a CTA.
 int decode_q8_tile_rows(int rows) { return rows <= 16 ? 16 : 32; }
 
-constexpr int kMaxWaves = 16;
-
-int q8_ctas_per_sm(int tile_rows) { return tile_rows == 16 ? Q8Smem<128, 1>::CTAS : Q8Smem<128, 2>::CTAS; }
-
-long long decode_q8_most_splits(long long problems, long long keys, int tile_rows, int sms) {
-  const long long rounds = (keys + kQ8Round - 1) / kQ8Round;
-  const long long fit = static_cast<long long>(sms) * q8_ctas_per_sm(tile_rows) * kMaxWaves / problems;
-  return fit < 1 ? 1 : (fit < rounds ? fit : rounds);
-}
-
-// Chunks of whole rounds of the warps (128 keys). A CTA's time is its rounds and
-// about kOverhead more (its start, its merge and its share of the join). For each
-// number of waves the chunks that just fill it are tried, and those that need
-// the least time in all are taken.
-void decode_q8_plan(long long problems, long long keys, int tile_rows, int sms, int* splits, int* chunk) {
-  constexpr long long kOverhead = 4;
-  const long long rounds = (keys + kQ8Round - 1) / kQ8Round;
-  const long long slots = static_cast<long long>(sms) * q8_ctas_per_sm(tile_rows);
-  const long long most = decode_q8_most_splits(problems, keys, tile_rows, sms);
-  long long per = rounds, least = ((problems + slots - 1) / slots) * (rounds + kOverhead / 2);
-  for (int w = 1; w <= kMaxWaves; ++w) {
-    long long n = slots * w / problems;
-    if (n > most) n = most;
-    if (n < 2) continue;
-    const long long r = (rounds + n - 1) / n;
-    const long long time = ((problems * ((rounds + r - 1) / r) + slots - 1) / slots) * (r + kOverhead);
-    if (time < least) {
-      least = time;
-      per = r;
-    }
-    if (n == most) break;
-  }
-  *splits = static_cast<int>((rounds + per - 1) / per);
-  *chunk = static_cast<int>(per * kQ8Round);
+// CTAs of a line (of `lines` KV heads and row tiles), the rounds that a piece has at
+// least, and whether each CTA takes one problem whole instead of a piece: where
+// none has more than kWhole rounds, dividing one and joining its parts takes
+// longer than it saves, and the second kernel is left out.
+void decode_q8_plan(long long problems, long long most_keys, int tile_rows, long long lines, int sms, int* ctas,
+                    int* least, int* whole) {
+  constexpr int kWhole = 4;
+  const long long slots = sms * (tile_rows == 16 ? Q8Smem<128, 1>::CTAS : Q8Smem<128, 2>::CTAS) / lines;
+  *whole = most_keys <= kWhole * kQ8Round;
+  *least = 2;
+  *ctas = static_cast<int>(*whole ? problems : (slots > 1 ? slots : 1));
 }
 
 cudaError_t launch_decode_q8(const DecodeQ8Params& p, cudaStream_t stream) {

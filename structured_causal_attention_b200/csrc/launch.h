@@ -104,25 +104,26 @@ struct DecodeQ8Params {
   const int32_t* seqlen;    // [B]
   __nv_bfloat16* o;         // [B, nq, Hq, D]
   float* lse;               // [B, Hq, nq]
-  float* part_o;            // [B, Hkv, groups, mt*tile_rows, splits, D] fp32
-  float* part_ml;           // [B, Hkv, groups, mt*tile_rows, splits, 2] fp32 (reference in log2 units, sum)
+  float* part_o;            // [mt, Hkv, slots, tile_rows, D] fp32
+  float* part_ml;           // [mt, Hkv, slots, tile_rows, 2] fp32 (reference in log2 units, sum)
   int* status;
   int B, n, Tcap, Hq, Hkv, D, g, nq, s0, groups, spg, kpt;  // g = Hq / Hkv
   int win;                  // keys of the window (kWinInf: none)
   int rows, tile_rows, mt;  // rows = spg*g, in mt tiles of tile_rows
-  int splits, chunk;        // chunk keys per split
+  // The line of rounds (of kQ8Round keys) of all problems of a KV head and row
+  // tile: ctas pieces of it, of `least` rounds and more; whole: a problem a CTA instead
+  int ctas, least, whole;
+  int slots;                // parts of a line: B * groups + ctas
   int format, bt, nb;
-  int step_stream, step_blk, step_off;  // how far 128 keys move a key's (stream, block, token in it)
+  int step_stream, step_blk, step_off;  // how far a round moves a key's (stream, block, token in it)
   float scale_log2;
-  FastDiv div_g, div_mt, div_splits, div_groups, div_hkv, div_rows, div_n, div_bt;
+  FastDiv div_g, div_mt, div_groups, div_hkv, div_rows, div_n, div_bt;
   long long ext_q, ext_lse, ext_scale, ext_part;
 };
 constexpr int kQ8Round = 128;  // keys that a CTA's warps take at once
 int decode_q8_tile_rows(int rows);
-// Splits and keys of one for `problems` (sequence, KV head, group, row tile) of up
-// to `keys` keys; fewer keys are never cut into more than most_splits of more.
-long long decode_q8_most_splits(long long problems, long long keys, int tile_rows, int sms);
-void decode_q8_plan(long long problems, long long keys, int tile_rows, int sms, int* splits, int* chunk);
+void decode_q8_plan(long long problems, long long most_keys, int tile_rows, long long lines, int sms, int* ctas,
+                    int* least, int* whole);
 cudaError_t launch_decode_q8(const DecodeQ8Params& p, cudaStream_t stream);
 
 struct RopeParams {
