@@ -9,16 +9,26 @@
 //   s_j = scale * ks_j * (q . kc_j),  O = sum_j softmax(s)_j vs_j vc_j
 //
 // Codes of both formats are exact in fp16, so the products run as fp16 MMAs on
-// converted codes and the scales stay outside, in fp32:
-//   - the query rows of a tile are multiplied by the power of two that puts the
-//     largest finite magnitude of them in [2^14, 2^15): exact but for elements
-//     2^29 and more below it, which keep an absolute error of 2^-40 of it;
-//   - the weight of a key is w_j = vs_j 2^(s_j - M), s in log2 units. M follows the
-//     running maximum of s + log2 vs: it is set so that the largest weight is
-//     2^13, and again once one passes 2^15, so that weights fit fp16 (rounding
-//     2^-12, kept down to 2^-27 of the largest). The softmax's sum takes the same
-//     weights without the scale, l += w_j / vs_j, in fp32. So blocks of very
-//     different size need no common scale, and O / l needs no correction.
+// converted codes, the scales outside in fp32. (An MMA on e4m3 operands is built
+// from fp16 ones here, with more conversions than these.) INT8's scores go to the
+// s8 MMA as they are, which takes half of fp16's time for a product and needs no
+// conversion; its weighted values do not, as a weight of two 8-bit terms keeps
+// 2^-17 of the largest, which the many small weights of a long cache add up to
+// more than. A query row's own scale rf:
+//   E4M3: the power of two that puts the row's largest magnitude in [2^14, 2^15),
+//         in fp16: exact but for elements 2^29 and more below it, which keep an
+//         error of 2^-40 of it.
+//   INT8: q = rf (256 hi + lo), q / rf rounded to a whole number, at most 32512:
+//         an error of 2^-16 of the row's largest, 2^-7 of what that one's own
+//         rounding to bf16 may be. The sums are exact: they start at 1.5 * 2^23 as
+//         bits, so that the whole number is read back as an fp32.
+//
+// With s in log2 units the weight of a key is w_j = vs_j 2^(s_j - M). M follows the
+// running maximum of s + log2 vs: it is set so that the largest weight is 2^13,
+// and again once one passes 2^15, so that weights fit fp16 (rounding 2^-12, kept
+// down to 2^-27 of the largest). The softmax's sum takes the same weights without
+// the scale, l += w_j / vs_j, in fp32. So blocks of very different size need no
+// common scale, and O / l needs no correction.
 //
 // Under INTRA each stream is a problem of its own (g query rows, every n-th
 // position), so every loaded key is visible and none is read twice; otherwise
@@ -53,18 +63,27 @@ constexpr int kQTile = 32;  // keys of a warp's tile
 static_assert(kQWarps * kQTile == kQ8Round, "a round");
 constexpr float kLn2 = 0.69314718055994530942f;
 
+// CTAs of an SM. Three hide more latency, but for E4M3 at D = 128, whose copies in
+// flight are then so many that HBM delivers less: 8 sequences of 16385 tokens took
+// 195 us with three and 176 with two (64 sequences, at the power cap's lower
+// clock: 1390 and 1520); INT8, with more to compute, 187 and 190 (1470 and 1540),
+// E4M3 at D = 64 105 and 118. Two row tiles need the registers of two.
+constexpr int q8_ctas_per_sm(int D, int format, int tile_rows) {
+  return tile_rows == 16 && (D == 64 || format == HD_Q8_INT8) ? 3 : 2;
+}
+
 // RT row tiles of 16 a CTA: the codes are converted once for all of them.
-template <int D, int RT>
+template <int D, int FMT, int RT>
 struct Q8Smem {
-  static constexpr int CTAS = RT == 1 ? 3 : 2;       // resident on an SM
+  static constexpr int CTAS = q8_ctas_per_sm(D, FMT, RT * 16);
   static constexpr int KV = kQTile * D;              // bytes of K (or V) of a tile
   static constexpr int STAGES = (RT == 1 ? 2 : 3) * (128 / D);
   static constexpr int RING = kQWarps * STAGES * 2 * KV;
-  static constexpr int Q = RT * 16 * D * 2;          // the query rows in fp16
+  static constexpr int Q = 2 * RT * 16 * D;          // the query rows: fp16, or two 8-bit terms
   static constexpr int FAC = kQWarps * kQTile * 12;  // per warp and key: score factor, log2 vs, 1/vs
   static constexpr int MERGE = kQWarps * RT * 16 * (D + 4) * 4;
   static constexpr int BARS = kQWarps * STAGES * 8;
-  static constexpr int TOTAL = RING + Q + FAC + BARS + 32 + 1024;  // and the alignment of the ring
+  static constexpr int TOTAL = RING + Q + FAC + BARS + RT * 64 + 16 + 1024;  // and the alignment of the ring
   static_assert(MERGE <= RING, "merge buffer");
 };
 
@@ -76,12 +95,28 @@ __device__ __forceinline__ uint32_t swz8(int row, int ch) {
   return D == 128 ? row * 128 + ((ch ^ (row & 7)) << 4) : row * 64 + ((ch ^ ((row >> 1) & 3)) << 4);
 }
 
+template <bool FIRST = false>
 __device__ __forceinline__ void mma_f16_16816(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
   asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-      "{%8,%9}, {%0,%1,%2,%3};\n"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};\n"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(FIRST ? 0.f : d[0]),
+        "f"(FIRST ? 0.f : d[1]), "f"(FIRST ? 0.f : d[2]), "f"(FIRST ? 0.f : d[3]));
+}
+
+// d += a b, 16 x 32 by 32 x 8 whole numbers, the sum as the bits of d; FIRST: d
+// starts at the bits of 1.5 * 2^23.
+template <bool FIRST>
+__device__ __forceinline__ void mma_s8_16832(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  int c[4], x[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) c[i] = FIRST ? 0x4b400000 : __float_as_int(d[i]);
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};\n"
+      : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "r"(c[0]), "r"(c[1]), "r"(c[2]), "r"(c[3]));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) d[i] = __int_as_float(x[i]);
 }
 
 // The codes in bytes (0, 1) and (2, 3) of r (PAIRS), or (0, 2) and (1, 3), as
@@ -114,6 +149,11 @@ __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
 __device__ __forceinline__ uint64_t f32x2_fma(uint64_t a, uint64_t b, uint64_t c) {
   uint64_t r;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t f32x2_mul(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
 __device__ __forceinline__ uint64_t f32x2_add(uint64_t a, uint64_t b) {
@@ -221,18 +261,18 @@ __device__ __forceinline__ Q8Line q8_line(const DecodeQ8Params& p, int lane) {
 }
 
 template <int D, int FMT, int RT>
-__global__ void __launch_bounds__(kQThreads, Q8Smem<D, RT>::CTAS)
+__global__ void __launch_bounds__(kQThreads, Q8Smem<D, FMT, RT>::CTAS)
     decode_q8_split_kernel(const DecodeQ8Params p, const __grid_constant__ CUtensorMap tmK,
                            const __grid_constant__ CUtensorMap tmV) {
-  using SM = Q8Smem<D, RT>;
-  constexpr int S = SM::STAGES, ROWS = 16 * RT, RCQ = D / 8;
+  using SM = Q8Smem<D, FMT, RT>;
+  constexpr int S = SM::STAGES, ROWS = 16 * RT;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t sRing = smem_u32(smem), sQ = sRing + SM::RING;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  int* after = reinterpret_cast<int*>(smem + SM::RING + SM::Q + SM::FAC + SM::BARS);
-  volatile int* abort_flag = after;
+  float* row_fac = reinterpret_cast<float*>(smem + SM::RING + SM::Q + SM::FAC + SM::BARS);  // [ROWS]
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(row_fac + ROWS);
   const uint32_t bars = sQ + SM::Q + SM::FAC + warp * S * 8;
   const uint32_t ring = sRing + warp * S * 2 * SM::KV;
   if (lane == 0) {
@@ -240,7 +280,11 @@ __global__ void __launch_bounds__(kQThreads, Q8Smem<D, RT>::CTAS)
     tc::fence_mbar_init();
     tc::fence_async_smem();
   }
-  if (tid == 0) *abort_flag = 0;
+  if (tid == 0) {
+    *abort_flag = 0;
+    tc::tma_prefetch_desc(&tmK);
+    tc::tma_prefetch_desc(&tmV);
+  }
   if (!p.whole) asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   const uint32_t line_head = p.div_mt.div(blockIdx.x);  // row tiles, then heads, side by side
   const int row0 = static_cast<int>(blockIdx.x - line_head * p.mt) * ROWS, valid_rows = min(ROWS, p.rows - row0);
@@ -327,47 +371,57 @@ __global__ void __launch_bounds__(kQThreads, Q8Smem<D, RT>::CTAS)
   };
   fetch_scales();
 
-  // ---- Q, as fp16 rows in shared memory. A register of an MMA's B operand holds
-  // four codes in a row of a key; so of the 16 k indexes of a step 2t, 2t+1, 2t+8,
-  // 2t+9 stand for d = 4t .. 4t+3.
-  float kfac;  // score factor: scale * log2(e) over the tile's power of two
-  {
-    constexpr int PER = ROWS * (D / 4) / kQThreads;
-    uint2 r[PER];
-    uint32_t am = 0;
+  // ---- Q: the rows in shared memory
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int lr = (tid + i * kQThreads) / (D / 4), d4 = (tid + i * kQThreads) % (D / 4);
-      r[i] = make_uint2(0, 0);  // rows past the last are zeros, and are not written
-      if (lr < valid_rows) {
-        const QRow qr = q_row(p, grp, hk, row0 + lr);
-        const long long qi = ((static_cast<long long>(b) * p.nq + qr.s) * p.Hq + qr.h) * D + d4 * 4;
-        if (in_bounds(qi, 4, p.ext_q, p.status)) r[i] = __ldg(reinterpret_cast<const uint2*>(p.q + qi));
+  for (int i = 0; i < ROWS * (D / 4) / kQThreads; ++i) {
+    const int lr = (tid + i * kQThreads) / (D / 4), d4 = (tid + i * kQThreads) % (D / 4);
+    uint2 r = make_uint2(0, 0);  // rows past the last are zeros, and are not written
+    if (lr < valid_rows) {
+      const QRow qr = q_row(p, grp, hk, row0 + lr);
+      const long long qi = ((static_cast<long long>(b) * p.nq + qr.s) * p.Hq + qr.h) * D + d4 * 4;
+      if (in_bounds(qi, 4, p.ext_q, p.status)) r = __ldg(reinterpret_cast<const uint2*>(p.q + qi));
+    }
+    uint32_t am = __vmaxu2(r.x & 0x7fff7fffu, r.y & 0x7fff7fffu);
+    am = __reduce_max_sync(D == 128 ? 0xffffffffu : 0xffffu << (lane & 16), max(am & 0xffffu, am >> 16));
+    const float x[4] = {__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xffff0000u), __uint_as_float(r.y << 16),
+                        __uint_as_float(r.y & 0xffff0000u)};
+    float fac;
+    uint32_t u, v;
+    if (FMT == HD_Q8_E4M3) {
+      // A register of an MMA's B operand holds four codes in a row of a key; so of
+      // the 16 k indexes of a step 2t, 2t+1, 2t+8, 2t+9 stand for d = 4t .. 4t+3.
+      const int up = min(14 - (max(static_cast<int>(am >> 7), 1) - 127), 126);
+      const float f = __int_as_float((up + 127) << 23);
+      fac = __int_as_float((127 - up) << 23);
+      u = pack_half(x[0] * f, x[1] * f);
+      v = pack_half(x[2] * f, x[3] * f);
+    } else {
+      const float top = fmaxf(__uint_as_float(am << 16), 1e-30f), f = 32512.f / top;
+      fac = top * (1.f / 32512.f);
+      u = v = 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int whole = min(max(__float2int_rn(x[k] * f), -32512), 32512), hi = (whole + 128) >> 8;
+        u |= static_cast<uint32_t>(hi & 0xff) << (8 * k);
+        v |= static_cast<uint32_t>((whole - 256 * hi) & 0xff) << (8 * k);
       }
-      const uint32_t u = r[i].x & 0x7fff7fffu, v = r[i].y & 0x7fff7fffu;
-      am = __vmaxu2(am, __vmaxu2(u & __vcmpltu2(u, 0x7f807f80u), v & __vcmpltu2(v, 0x7f807f80u)));
     }
-    am = __reduce_max_sync(0xffffffffu, max(am & 0xffffu, am >> 16));
-    if (lane == 0) after[1 + warp] = static_cast<int>(am);
-    __syncthreads();
-    am = 0;
-#pragma unroll
-    for (int w = 0; w < kQWarps; ++w) am = max(am, static_cast<uint32_t>(after[1 + w]));
-    const int e = max(static_cast<int>(am >> 7), 1) - 127;
-    const int up = min(max(14 - e, -126), 126);
-    const float f = __int_as_float((up + 127) << 23);
-    kfac = p.scale_log2 * __int_as_float((127 - up) << 23);
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int lr = (tid + i * kQThreads) / (D / 4), d4 = (tid + i * kQThreads) % (D / 4);
-      const uint32_t lo = pack_half(__uint_as_float(r[i].x << 16) * f, __uint_as_float(r[i].x & 0xffff0000u) * f);
-      const uint32_t hi = pack_half(__uint_as_float(r[i].y << 16) * f, __uint_as_float(r[i].y & 0xffff0000u) * f);
-      const uint32_t at = (d4 & 3) * 4;
-      asm volatile("st.shared.b32 [%0], %1;\n" ::"r"(sQ + swz(lr, (d4 >> 2) * 2, RCQ) + at), "r"(lo) : "memory");
-      asm volatile("st.shared.b32 [%0], %1;\n" ::"r"(sQ + swz(lr, (d4 >> 2) * 2 + 1, RCQ) + at), "r"(hi) : "memory");
+    if (am >= 0x7f80u) {  // an infinity or NaN: so is every score of the row
+      fac = __int_as_float(0x7fffffff);
+      u = v = 0;
     }
-    __syncthreads();
+    const uint32_t at_u = FMT == HD_Q8_E4M3 ? swz(lr, (d4 >> 2) * 2, D / 8) : swz8<D>(lr, d4 >> 2);
+    const uint32_t at_v = FMT == HD_Q8_E4M3 ? swz(lr, (d4 >> 2) * 2 + 1, D / 8) : at_u + ROWS * D;
+    asm volatile("st.shared.b32 [%0], %1;\n" ::"r"(sQ + at_u + (d4 & 3) * 4), "r"(u) : "memory");
+    asm volatile("st.shared.b32 [%0], %1;\n" ::"r"(sQ + at_v + (d4 & 3) * 4), "r"(v) : "memory");
+    if (d4 == 0) row_fac[lr] = fac;
   }
+  __syncthreads();
+  float rf[RT][2];
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+    for (int hr = 0; hr < 2; ++hr) rf[rt][hr] = row_fac[rt * 16 + (lane >> 2) + hr * 8];
 
   // o[rt][c][h]: d = c*16 + 4t + h and + 2 + h (h = 0, 1) of rows lane/4, lane/4 + 8
   float o[RT][D / 16][2][4];
@@ -395,7 +449,7 @@ __global__ void __launch_bounds__(kQThreads, Q8Smem<D, RT>::CTAS)
       const bool fin = e < 128 && e > -127;
       // A scale that is no number (its block took in one) makes the scores of its
       // visible keys NaN. One of zero (never written) counts as the smallest.
-      fac[lane] = ks * kfac;
+      fac[lane] = ks * p.scale_log2;
       fac[kQTile + lane] = fin ? static_cast<float>(e) + __log2f(__uint_as_float((vbits & 0x007fffffu) | 0x3f800000u))
                                : (e == 128 ? __int_as_float(0x7fffffff) : static_cast<float>(kQ8MinExp));
       fac[2 * kQTile + lane] = fin ? __fdividef(1.f, vs) : (e == 128 ? 1.f : __int_as_float((127 - kQ8MinExp) << 23));
@@ -411,31 +465,52 @@ __global__ void __launch_bounds__(kQThreads, Q8Smem<D, RT>::CTAS)
     }
     __syncwarp();
 
-    float s[RT][kQTile / 8][4];
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-      for (int j = 0; j < kQTile / 8; ++j) s[rt][j][0] = s[rt][j][1] = s[rt][j][2] = s[rt][j][3] = 0.f;
+    float s[RT][FMT == HD_Q8_E4M3 ? 1 : 2][kQTile / 8][4];  // (of each term)
 #pragma unroll
     for (int c4 = 0; c4 < D / 16; c4 += 4) {
       uint32_t r[kQTile / 8][4];
 #pragma unroll
       for (int j = 0; j < kQTile / 8; ++j)  // 8 keys, 64 of d
         ldsm_x4(kb + swz8<D>(j * 8 + (lane & 7), c4 + (lane >> 3)), r[j][0], r[j][1], r[j][2], r[j][3]);
+      if constexpr (FMT == HD_Q8_E4M3) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t qf[RT][4];
+        for (int i = 0; i < 4; ++i) {
+          uint32_t qf[RT][4];
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
-          ldsm_x4(sQ + swz(rt * 16 + (lane & 15), (c4 + i) * 2 + (lane >> 4), RCQ), qf[rt][0], qf[rt][1], qf[rt][2],
-                  qf[rt][3]);
+          for (int rt = 0; rt < RT; ++rt)
+            ldsm_x4(sQ + swz(rt * 16 + (lane & 15), (c4 + i) * 2 + (lane >> 4), D / 8), qf[rt][0], qf[rt][1],
+                    qf[rt][2], qf[rt][3]);
 #pragma unroll
-        for (int j = 0; j < kQTile / 8; ++j) {
-          uint32_t b0, b1;
-          to_half<FMT, true>(r[j][i], b0, b1);
+          for (int j = 0; j < kQTile / 8; ++j) {
+            uint32_t b0, b1;
+            to_half<FMT, true>(r[j][i], b0, b1);
 #pragma unroll
-          for (int rt = 0; rt < RT; ++rt) mma_f16_16816(s[rt][j], qf[rt], b0, b1);
+            for (int rt = 0; rt < RT; ++rt) {
+              if (c4 + i == 0)
+                mma_f16_16816<true>(s[rt][0][j], qf[rt], b0, b1);
+              else
+                mma_f16_16816(s[rt][0][j], qf[rt], b0, b1);
+            }
+          }
         }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; i += 2)
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int term = 0; term < 2; ++term) {
+              uint32_t qf[4];
+              ldsm_x4(sQ + term * (ROWS * D) + swz8<D>(rt * 16 + (lane & 15), c4 + i + (lane >> 4)), qf[0], qf[1],
+                      qf[2], qf[3]);
+#pragma unroll
+              for (int j = 0; j < kQTile / 8; ++j) {
+                if (c4 + i == 0)
+                  mma_s8_16832<true>(s[rt][term][j], qf, r[j][i], r[j][i + 1]);
+                else
+                  mma_s8_16832<false>(s[rt][term][j], qf, r[j][i], r[j][i + 1]);
+              }
+            }
       }
     }
     const bool all_seen = base + kQTile <= ce && base + kQTile - 1 <= pmin && pmax - base < p.win;
@@ -443,15 +518,23 @@ __global__ void __launch_bounds__(kQThreads, Q8Smem<D, RT>::CTAS)
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
       float mx[2] = {-INFINITY, -INFINITY};
+      const uint64_t rf2[2] = {pack_f32x2(rf[rt][0], rf[rt][0]), pack_f32x2(rf[rt][1], rf[rt][1])};
 #pragma unroll
       for (int j = 0; j < kQTile / 8; ++j) {
         const uint32_t at = sFac + (j * 8 + (lane & 3) * 2) * 4;
         const uint64_t f = lds64(at), lv = lds64(at + kQTile * 4);
 #pragma unroll
         for (int hr = 0; hr < 2; ++hr) {
-          const float2 x = f32x2_parts(f32x2_fma(pack_f32x2(s[rt][j][2 * hr], s[rt][j][2 * hr + 1]), f, lv));
-          s[rt][j][2 * hr] = x.x;
-          s[rt][j][2 * hr + 1] = x.y;
+          uint64_t dot = pack_f32x2(s[rt][0][j][2 * hr], s[rt][0][j][2 * hr + 1]);
+          if constexpr (FMT == HD_Q8_INT8) {
+            constexpr float kLess = -1.5f * (1 << 23);
+            const uint64_t less = pack_f32x2(kLess, kLess), weigh = pack_f32x2(256.f, 256.f);
+            const uint64_t lo = pack_f32x2(s[rt][1][j][2 * hr], s[rt][1][j][2 * hr + 1]);
+            dot = f32x2_fma(f32x2_add(dot, less), weigh, f32x2_add(lo, less));
+          }
+          const float2 x = f32x2_parts(f32x2_fma(f32x2_mul(dot, rf2[hr]), f, lv));
+          s[rt][0][j][2 * hr] = x.x;
+          s[rt][0][j][2 * hr + 1] = x.y;
         }
       }
       if (!all_seen) {
@@ -464,14 +547,14 @@ __global__ void __launch_bounds__(kQThreads, Q8Smem<D, RT>::CTAS)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const int c = base + j * 8 + (lane & 3) * 2 + e;
-              if (!(c < ce && c <= own && own - c < p.win)) s[rt][j][2 * hr + e] = -INFINITY;
+              if (!(c < ce && c <= own && own - c < p.win)) s[rt][0][j][2 * hr + e] = -INFINITY;
             }
         }
       }
 #pragma unroll
       for (int j = 0; j < kQTile / 8; ++j)
 #pragma unroll
-        for (int hr = 0; hr < 2; ++hr) mx[hr] = fmaxf(mx[hr], fmaxf(s[rt][j][2 * hr], s[rt][j][2 * hr + 1]));
+        for (int hr = 0; hr < 2; ++hr) mx[hr] = fmaxf(mx[hr], fmaxf(s[rt][0][j][2 * hr], s[rt][0][j][2 * hr + 1]));
       if (__any_sync(0xffffffffu, mx[0] > m_run[rt][0] + 15.f || mx[1] > m_run[rt][1] + 15.f)) {
 #pragma unroll
         for (int hr = 0; hr < 2; ++hr) {
@@ -499,7 +582,7 @@ __global__ void __launch_bounds__(kQThreads, Q8Smem<D, RT>::CTAS)
 #pragma unroll
         for (int j = 0; j < kQTile / 8; ++j) {
           const uint64_t iv = lds64(sFac + (2 * kQTile + j * 8 + (lane & 3) * 2) * 4);
-          const float2 x = f32x2_parts(f32x2_add(pack_f32x2(s[rt][j][2 * hr], s[rt][j][2 * hr + 1]), mu2));
+          const float2 x = f32x2_parts(f32x2_add(pack_f32x2(s[rt][0][j][2 * hr], s[rt][0][j][2 * hr + 1]), mu2));
           const float w0 = fast_exp2(x.x), w1 = fast_exp2(x.y);
           l_run[rt][hr] = f32x2_fma(pack_f32x2(w0, w1), iv, l_run[rt][hr]);
           a[rt][j / 2][2 * (j & 1) + hr] = pack_half(w0, w1);
@@ -607,15 +690,16 @@ __global__ void __launch_bounds__(kQThreads, Q8Smem<D, RT>::CTAS)
   }
 }
 
-// The pieces of a query row joined, one CTA a row: its groups of D / 4 threads
-// take the pieces in turn. Launched while the first kernel still runs; what that
-// wrote is there once griddepcontrol.wait returns.
+// The parts of a query row joined, one CTA a row: its groups of D / 4 threads
+// take the parts in turn, each with a running reference of its own, so that a
+// part's reference and values are loaded side by side. Launched while the first
+// kernel still runs; what that wrote is there once griddepcontrol.wait returns.
 template <int D>
 __global__ void __launch_bounds__(kQThreads) decode_q8_combine_kernel(const DecodeQ8Params p) {
   constexpr int LPR = D / 4, G = kQThreads / LPR;
-  __shared__ float red[2][kQWarps];
+  __shared__ float2 ref[G];
   __shared__ float4 sum[G][LPR];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
   const uint32_t unit = p.div_rows.div(blockIdx.x);
   const int row = static_cast<int>(blockIdx.x - unit * p.rows);
   const int prob = static_cast<int>(p.div_hkv.div(unit)), hk = static_cast<int>(unit) - prob * p.Hkv;
@@ -638,51 +722,64 @@ __global__ void __launch_bounds__(kQThreads) decode_q8_combine_kernel(const Deco
   if (!in_bounds(first, (parts - 1) * step + 1, p.ext_part, p.status) || !in_bounds(orow * D, D, p.ext_q, p.status) ||
       !in_bounds(li, 1, p.ext_lse, p.status))
     return;
-  const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + first;
-  float mx = -INFINITY;
-  for (int j = tid; j < parts; j += kQThreads) mx = fmaxf(mx, ml[j * step].x);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  if (lane == 0) red[0][warp] = mx;
-  __syncthreads();
-  mx = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
-  const float mu = (mx == -INFINITY) ? 0.f : mx;
-  float lt = 0.f;
-  for (int j = tid; j < parts; j += kQThreads) {
-    const float2 x = ml[j * step];
-    lt += fast_exp2(x.x - mu) * x.y;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) lt += __shfl_xor_sync(0xffffffffu, lt, o);
-  if (lane == 0) red[1][warp] = lt;
+  float m = -INFINITY, l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int j = tid / LPR; j < parts; j += G) {
-    // (a piece without a key that the row sees has reference -inf and sum 0)
-    const float f = fast_exp2(ml[j * step].x - mu);
-    const float4 v = *reinterpret_cast<const float4*>(p.part_o + (first + j * step) * D + (tid % LPR) * 4);
-    acc.x += f * v.x;
-    acc.y += f * v.y;
-    acc.z += f * v.z;
-    acc.w += f * v.w;
+  constexpr int U = 4;  // parts in flight
+  for (int j0 = tid / LPR; j0 < parts; j0 += U * G) {
+    float2 ml[U];
+    float4 v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      // (a part without a key that the row sees has reference -inf, sum 0 and values 0)
+      ml[u] = make_float2(-INFINITY, 0.f);
+      v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      const long long at = first + (j0 + u * G) * step;
+      if (j0 + u * G < parts) {
+        ml[u] = reinterpret_cast<const float2*>(p.part_ml)[at];
+        v[u] = *reinterpret_cast<const float4*>(p.part_o + at * D + (tid % LPR) * 4);
+      }
+    }
+    float top = m;
+#pragma unroll
+    for (int u = 0; u < U; ++u) top = fmaxf(top, ml[u].x);
+    const float mu = top == -INFINITY ? 0.f : top, f = fast_exp2(m - mu);
+    m = top;
+    l *= f;
+    acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const float g = fast_exp2(ml[u].x - mu);
+      l += g * ml[u].y;
+      acc.x += g * v[u].x;
+      acc.y += g * v[u].y;
+      acc.z += g * v[u].z;
+      acc.w += g * v[u].w;
+    }
   }
+  if (tid % LPR == 0) ref[tid / LPR] = make_float2(m, l);
   sum[tid / LPR][tid % LPR] = acc;
   __syncthreads();
-  lt = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
-  if (tid < LPR) {
+  if (tid >= LPR) return;
+  float top = -INFINITY;
 #pragma unroll
-    for (int i = 1; i < G; ++i) {
-      const float4 v = sum[i][tid];
-      acc.x += v.x;
-      acc.y += v.y;
-      acc.z += v.z;
-      acc.w += v.w;
-    }
-    const float inv = 1.f / lt;
-    *reinterpret_cast<uint2*>(p.o + orow * D + tid * 4) =
-        make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-    if (tid == 0) p.lse[li] = (mx + __log2f(lt)) * kLn2;
+  for (int i = 0; i < G; ++i) top = fmaxf(top, ref[i].x);
+  const float mu = top == -INFINITY ? 0.f : top;
+  l = 0.f;
+  acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int i = 0; i < G; ++i) {
+    const float g = fast_exp2(ref[i].x - mu);
+    const float4 v = sum[i][tid];
+    l += g * ref[i].y;
+    acc.x += g * v.x;
+    acc.y += g * v.y;
+    acc.z += g * v.z;
+    acc.w += g * v.w;
   }
+  const float inv = 1.f / l;
+  *reinterpret_cast<uint2*>(p.o + orow * D + tid * 4) =
+      make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+  if (tid == 0) p.lse[li] = (top + __log2f(l)) * kLn2;
 }
 
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
@@ -725,7 +822,7 @@ cudaError_t launch_decode_q8_d(const DecodeQ8Params& p, cudaStream_t stream) {
   const long long R = intra ? p.Tcap : static_cast<long long>(p.Tcap) * p.n;
   CUtensorMap mk, mv;
   if (!make_map<D>(&mk, p.kc, J, R, p.B) || !make_map<D>(&mv, p.vc, J, R, p.B)) return cudaErrorInvalidValue;
-  const int smem = Q8Smem<D, RT>::TOTAL;
+  const int smem = Q8Smem<D, FMT, RT>::TOTAL;
   cudaError_t e = cudaFuncSetAttribute(decode_q8_split_kernel<D, FMT, RT>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
@@ -760,10 +857,10 @@ int decode_q8_tile_rows(int rows) { return rows <= 16 ? 16 : 32; }
 // least, and whether each CTA takes one problem whole instead of a piece: where
 // none has more than kWhole rounds, dividing one and joining its parts takes
 // longer than it saves, and the second kernel is left out.
-void decode_q8_plan(long long problems, long long most_keys, int tile_rows, long long lines, int sms, int* ctas,
+void decode_q8_plan(long long problems, long long most_keys, int D, int format, int tile_rows, long long lines, int sms, int* ctas,
                     int* least, int* whole) {
-  constexpr int kWhole = 4;
-  const long long slots = sms * (tile_rows == 16 ? Q8Smem<128, 1>::CTAS : Q8Smem<128, 2>::CTAS) / lines;
+  constexpr int kWhole = 8;
+  const long long slots = sms * q8_ctas_per_sm(D, format, tile_rows) / lines;
   *whole = most_keys <= kWhole * kQ8Round;
   *least = 2;
   *ctas = static_cast<int>(*whole ? problems : (slots > 1 ? slots : 1));
