@@ -284,16 +284,22 @@ def _cache_q8(cache):
     return B, Tcap, Hkv, D, HD_Q8_E4M3 if k.dtype == torch.float8_e4m3fn else HD_Q8_INT8
 
 
-def _on(device, *ts):
-    """The tensors' one device as the current one: a context."""
+def _one_device(*ts):
+    """The index of the tensors' one device (``None`` among them is passed over)."""
+    first = ts[0].get_device()
+    for t in ts:
+        if t is not None and t.get_device() != first:
+            raise ValueError("tensors must live on one device")
+    return first
+
+
+def _on(index):
+    """Device ``index`` as the current one: a context."""
     import contextlib
 
     import torch
 
-    for t in ts:
-        if t is not None and t.device != device:
-            raise ValueError("tensors must live on one device")
-    return contextlib.nullcontext() if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+    return contextlib.nullcontext() if index == torch.cuda.current_device() else torch.cuda.device(index)
 
 
 def _index_q8(t, B, what):
@@ -319,7 +325,7 @@ def kv_write_q8(k, v, cache, token_offset=None, lengths=None, stream=None):
     _index_q8(token_offset, B, "token_offset")
     _index_q8(lengths, B, "lengths")
     L = k.shape[1] // cache.n
-    with _on(cache.k.device, cache.v, cache.k_scale, cache.v_scale, k, v, token_offset, lengths):
+    with _on(_one_device(cache.k, cache.v, cache.k_scale, cache.v_scale, k, v, token_offset, lengths)):
         if L:
             hd_kv_write_q8(k, v, token_offset, lengths, cache.k, cache.v, cache.k_scale, cache.v_scale, B, L,
                            cache.n, Tcap, Hkv, D, fmt, cache.block_tokens, stream)
@@ -340,7 +346,7 @@ def kv_read_q8(cache, L, token_offset=None, lengths=None, out=None, stream=None)
     _need_cuda(k, v)
     if k.dtype != torch.bfloat16 or v.dtype != torch.bfloat16 or k.shape != shape or v.shape != shape:
         raise ValueError(f"out must be two bfloat16 tensors {list(shape)}")
-    with _on(cache.k.device, cache.v, cache.k_scale, cache.v_scale, token_offset, lengths, k, v):
+    with _on(_one_device(cache.k, cache.v, cache.k_scale, cache.v_scale, token_offset, lengths, k, v)):
         if L:
             hd_kv_read_q8(cache.k, cache.v, cache.k_scale, cache.v_scale, token_offset, lengths, k, v, B, L,
                           cache.n, Tcap, Hkv, D, fmt, cache.block_tokens, stream)
@@ -362,7 +368,7 @@ def _decode_q8(q, cache, seqlen, mode, W, scale, stream, workspace, final):
     Hq = q.shape[2]
     if scale is None:
         scale = D ** -0.5
-    with _on(q.device, cache.k, cache.v, cache.k_scale, cache.v_scale, seqlen, workspace):
+    with _on(_one_device(q, cache.k, cache.v, cache.k_scale, cache.v_scale, seqlen, workspace)):
         out = torch.empty_like(q)
         lse = q.new_empty((B, Hq, nq), dtype=torch.float32)
         if workspace is None:

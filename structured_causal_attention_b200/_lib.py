@@ -108,11 +108,10 @@ def status_string(status: int) -> str:
 
 def ptr(x) -> int:
     """Device pointer of a tensor (or an int passed through); None -> 0."""
-    if x is None:
-        return 0
-    if isinstance(x, int):
-        return x
-    return int(x.data_ptr())
+    try:
+        return x.data_ptr()
+    except AttributeError:
+        return 0 if x is None else x
 
 
 def stream_handle(stream) -> int:

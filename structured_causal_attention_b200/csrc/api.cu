@@ -253,8 +253,8 @@ int kv_q8_params(KvQ8Params& p, const int32_t* token_offset, const int32_t* leng
   p.nb = q8_blocks(Tcap, block_tokens);
   // L tokens touch the most blocks when they begin at a block's last token
   p.blocks = token_offset ? q8_blocks(L - 1, block_tokens) + 1 : q8_blocks(L, block_tokens);
-  // units of a sequence are counted in 32 bits: (block, stream, head) of a write, 8 elements of a read
-  if (static_cast<long long>(p.blocks) * n * Hkv > (1LL << 31) - 1024 ||
+  // counted in 32 bits of a sequence: warps of a write (at most 8 a block, stream and head), 8 elements of a read
+  if (static_cast<long long>(p.blocks) * n * Hkv > (1LL << 28) ||
       static_cast<long long>(L) * n * Hkv * (D / 8) > (1LL << 31) - 1024)
     return HD_ERR_UNSUPPORTED;
   p.div_hkv = FastDiv::by(static_cast<uint32_t>(Hkv));

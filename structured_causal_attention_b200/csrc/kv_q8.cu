@@ -19,11 +19,12 @@
 // are then rounded again; it is never lowered, so nothing is rounded twice
 // unless the range grew.
 //
-// Writing: one warp owns one (K or V, sequence, block, stream, head): it alone
-// reads and writes that scale and those codes, so no atomics and no order
-// between warps. It holds its block's rows in registers between finding their
-// largest magnitude and storing their codes, so each row is read once. Rows of
-// neighbouring heads are neighbours in memory and so are their warps.
+// Writing: one warp, or for long blocks a few of a CTA, own one (K or V, sequence,
+// block, stream, head): they alone read and write that scale and those codes, so
+// no atomics and no order between units. They hold the block's rows in registers
+// between finding their largest magnitude and storing their codes, so each row is
+// read once. Rows of neighbouring heads are neighbours in memory and so are their
+// warps.
 // Reading: eight codes a thread, four such in flight.
 #include <cuda_fp8.h>
 
@@ -105,6 +106,11 @@ __device__ __forceinline__ uint32_t requantise4(uint32_t c, float old, float now
   return r;
 }
 
+// A barrier of the `count` warps from warp `first` on.
+__device__ __forceinline__ void unit_sync(int first, int count) {
+  asm volatile("bar.sync %0, %1;\n" ::"r"(1 + first), "r"(count * 32) : "memory");
+}
+
 // The range [t0, t0 + len) of sequence b, or false (and the status word) if it
 // does not lie in the cache or is longer than the rows given.
 __device__ __forceinline__ bool token_range(const KvQ8Params& p, int b, int& t0, int& len, bool report) {
@@ -115,18 +121,21 @@ __device__ __forceinline__ bool token_range(const KvQ8Params& p, int b, int& t0,
   return false;
 }
 
-// NP: passes (of 32 * 8 / D rows) held in registers; longer blocks are read a
-// second time for their codes.
+// NP: passes (of 32 * 8 / D rows) that a warp holds in registers; p.wpu warps have
+// a unit. Blocks longer than that are read a second time for their codes.
 template <int D, int FMT, int NP>
-__global__ void __launch_bounds__(kKvWarps * 32) kv_write_q8_kernel(const KvQ8Params p) {
+__global__ void __launch_bounds__(kKvWarps * 32, NP == 8 ? 3 : 5) kv_write_q8_kernel(const KvQ8Params p) {
   constexpr int LPR = D / 8;      // lanes of a row, eight elements each
   constexpr int RPP = 32 / LPR;   // rows of a pass
-  const int lane = threadIdx.x & 31, sub = lane / LPR, col = (lane % LPR) * 8;
+  __shared__ uint32_t largest_of[kKvWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, col = (lane % LPR) * 8;
+  const int unit0 = warp / p.wpu * p.wpu;  // the unit's first warp
+  const int sub = (warp - unit0) * RPP + lane / LPR, step = p.wpu * RPP;
   const bool is_v = blockIdx.z != 0;
   const __nv_bfloat16* x = is_v ? p.v : p.k;
   uint8_t* codes = is_v ? p.v_codes : p.k_codes;
   float* scales = is_v ? p.v_scale : p.k_scale;
-  const uint32_t unit = blockIdx.x * kKvWarps + (threadIdx.x >> 5);
+  const uint32_t unit = (blockIdx.x * kKvWarps + warp) / p.wpu;
   const uint32_t bs = p.div_hkv.div(unit);
   const int hk = static_cast<int>(unit - bs * p.Hkv);
   const int jb = static_cast<int>(p.div_n.div(bs));
@@ -144,10 +153,10 @@ __global__ void __launch_bounds__(kKvWarps * 32) kv_write_q8_kernel(const KvQ8Pa
     const long long at = (static_cast<long long>(s) * p.Hkv + hk) * D + col;
     const long long xo = (static_cast<long long>(b) * p.L - t0) * tstep + at;
     const long long co = static_cast<long long>(b) * p.Tcap * tstep + at;
+    const long long xstep = step * tstep;  // from one row of a thread to its next
     const long long si = ((static_cast<long long>(b) * p.Hkv + hk) * p.nb + blk) * p.n + s;
     if (!in_bounds(si, 1, p.ext_scale, p.status)) continue;
-    auto row = [&](int t) {
-      const long long o = xo + t * tstep;
+    auto row = [&](int t, long long o) {
       if (t >= end || !in_bounds(o, 8, p.ext_rows, p.status)) return make_uint4(0, 0, 0, 0);
       return __ldg(reinterpret_cast<const uint4*>(x + o));
     };
@@ -159,19 +168,27 @@ __global__ void __launch_bounds__(kKvWarps * 32) kv_write_q8_kernel(const KvQ8Pa
     const float old = first < t0 ? scales[si] : 0.f;
     uint4 held[NP];
     uint32_t am = 0;
+    const int t1 = lo + sub;
+    long long at_x = xo + t1 * tstep;
 #pragma unroll
-    for (int i = 0; i < NP; ++i) held[i] = row(lo + sub + i * RPP);
+    for (int i = 0; i < NP; ++i, at_x += xstep) held[i] = row(t1 + i * step, at_x);
 #pragma unroll
     for (int i = 0; i < NP; ++i) am = largest(am, held[i]);
-    for (int t = lo + sub + NP * RPP; t < end; t += RPP) am = largest(am, row(t));
-    const uint32_t abits = __reduce_max_sync(0xffffffffu, max(am & 0xffffu, am >> 16));
+    for (int t = t1 + NP * step; t < end; t += step) am = largest(am, row(t, xo + t * tstep));
+    uint32_t abits = __reduce_max_sync(0xffffffffu, max(am & 0xffffu, am >> 16));
+    if (p.wpu > 1) {  // (all warps of a unit take the same branches)
+      if (lane == 0) largest_of[warp] = abits;
+      unit_sync(unit0, p.wpu);
+      abits = __reduce_max_sync(0xffffffffu, lane < p.wpu ? largest_of[unit0 + lane] : 0u);
+      unit_sync(unit0, p.wpu);
+    }
     const bool finite = abits < 0x7f80u;
     float now = finite ? fmaxf(scale_for<FMT>(abits), old) : __int_as_float(0x7fffffff);
     if (old != old) now = old;
     const bool poison = now != now;
-    if (lane == 0) scales[si] = now;  // every lane's read of the old one is before the reduction
+    if (warp == unit0 && lane == 0) scales[si] = now;  // every lane's read of the old one is before the reduction
     if (first < t0 && now > old) {
-      for (int t = static_cast<int>(first) + sub; t < lo; t += RPP) {
+      for (int t = static_cast<int>(first) + sub; t < lo; t += step) {
         const long long o = co + t * tstep;
         if (!in_bounds(o, 8, p.ext_codes, p.status)) continue;
         uint2* c = reinterpret_cast<uint2*>(codes + o);
@@ -180,15 +197,15 @@ __global__ void __launch_bounds__(kKvWarps * 32) kv_write_q8_kernel(const KvQ8Pa
       }
     }
     const float inv = __fdiv_rn(1.f, now);
-    auto store = [&](int t, const uint4& r) {
-      const long long o = co + t * tstep;
+    auto store = [&](int t, long long o, const uint4& r) {
       if (t >= end || !in_bounds(o, 8, p.ext_codes, p.status)) return;
       *reinterpret_cast<uint2*>(codes + o) =
           poison ? make_uint2(0, 0) : make_uint2(quantise4<FMT>(r.x, r.y, inv), quantise4<FMT>(r.z, r.w, inv));
     };
+    long long at_c = co + t1 * tstep;
 #pragma unroll
-    for (int i = 0; i < NP; ++i) store(lo + sub + i * RPP, held[i]);
-    for (int t = lo + sub + NP * RPP; t < end; t += RPP) store(t, row(t));
+    for (int i = 0; i < NP; ++i, at_c += xstep) store(t1 + i * step, at_c, held[i]);
+    for (int t = t1 + NP * step; t < end; t += step) store(t, co + t * tstep, row(t, xo + t * tstep));
   }
 }
 
@@ -248,17 +265,20 @@ dim3 kv_grid(long long x, int B) {
 }
 
 template <int D, int FMT>
-cudaError_t launch_write_d(const KvQ8Params& p, cudaStream_t stream) {
+cudaError_t launch_write_d(KvQ8Params p, cudaStream_t stream) {
   constexpr int RPP = 32 * 8 / D;
-  const dim3 grid = kv_grid((static_cast<long long>(p.blocks) * p.n * p.Hkv + kKvWarps - 1) / kKvWarps, p.B);
-  // rows of a block that can be new in one call
+  // rows of a block that can be new in one call, eight passes of them a warp
   const int rows = p.bt < p.L ? p.bt : p.L;
+  p.wpu = 1;
+  while (p.wpu < kKvWarps && rows > p.wpu * 8 * RPP) p.wpu *= 2;
+  const long long warps = static_cast<long long>(p.blocks) * p.n * p.Hkv * p.wpu;
+  const dim3 grid = kv_grid((warps + kKvWarps - 1) / kKvWarps, p.B);
   if (rows <= 2 * RPP)
     kv_write_q8_kernel<D, FMT, 2><<<grid, kKvWarps * 32, 0, stream>>>(p);
-  else if (rows <= 8 * RPP)
-    kv_write_q8_kernel<D, FMT, 8><<<grid, kKvWarps * 32, 0, stream>>>(p);
+  else if (rows <= 4 * RPP)
+    kv_write_q8_kernel<D, FMT, 4><<<grid, kKvWarps * 32, 0, stream>>>(p);
   else
-    kv_write_q8_kernel<D, FMT, 16><<<grid, kKvWarps * 32, 0, stream>>>(p);
+    kv_write_q8_kernel<D, FMT, 8><<<grid, kKvWarps * 32, 0, stream>>>(p);
   return cudaGetLastError();
 }
 

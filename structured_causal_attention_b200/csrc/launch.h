@@ -84,6 +84,7 @@ struct KvQ8Params {
   int* status;
   int B, L, n, Tcap, Hkv, D, format, bt, nb;  // nb = blocks of bt tokens in Tcap
   int blocks;              // blocks that L tokens can touch
+  int wpu;                 // warps of a (block, stream, head) of a write (set by the launcher)
   FastDiv div_hkv, div_n, div_bt;
   // allocated elements, for the checked build's bounds checks
   long long ext_rows, ext_codes, ext_scale;
