@@ -9,19 +9,13 @@
 //   s_j = scale * ks_j * (q . kc_j),  O = sum_j softmax(s)_j vs_j vc_j
 //
 // Codes of both formats are exact in fp16, so the products run as fp16 MMAs on
-// converted codes, the scales outside in fp32. (An MMA on e4m3 operands is built
-// from fp16 ones here, with more conversions than these.) INT8's scores go to the
-// s8 MMA as they are, which takes half of fp16's time for a product and needs no
-// conversion; its weighted values do not, as a weight of two 8-bit terms keeps
-// 2^-17 of the largest, which the many small weights of a long cache add up to
-// more than. A query row's own scale rf:
-//   E4M3: the power of two that puts the row's largest magnitude in [2^14, 2^15),
-//         in fp16: exact but for elements 2^29 and more below it, which keep an
-//         error of 2^-40 of it.
-//   INT8: q = rf (256 hi + lo), q / rf rounded to a whole number, at most 32512:
-//         an error of 2^-16 of the row's largest, 2^-7 of what that one's own
-//         rounding to bf16 may be. The sums are exact: they start at 1.5 * 2^23 as
-//         bits, so that the whole number is read back as an fp32.
+// converted codes, the scales outside in fp32. (The 8-bit MMAs were built and
+// measured. One on e4m3 operands is made of an fp16 one here and converts them
+// itself, the query's terms too: 196 us became 228. INT8's scores on the s8 MMA,
+// with a query of two 8-bit terms, are 2-5% faster, but an error of 2^-16 of a
+// row's largest element is too much for its lse.) A query row is multiplied by the
+// power of two that puts its largest magnitude in [2^14, 2^15): exact but for
+// elements 2^29 and more below it, which keep an error of 2^-40 of it.
 //
 // With s in log2 units the weight of a key is w_j = vs_j 2^(s_j - M). M follows the
 // running maximum of s + log2 vs: it is set so that the largest weight is 2^13,
@@ -66,8 +60,8 @@ constexpr float kLn2 = 0.69314718055994530942f;
 // CTAs of an SM. Three hide more latency, but for E4M3 at D = 128, whose copies in
 // flight are then so many that HBM delivers less: 8 sequences of 16385 tokens took
 // 195 us with three and 176 with two (64 sequences, at the power cap's lower
-// clock: 1390 and 1520); INT8, with more to compute, 187 and 190 (1470 and 1540),
-// E4M3 at D = 64 105 and 118. Two row tiles need the registers of two.
+// clock: 1390 and 1520); INT8, with more to compute, 186 and 196 (1550 and 1740), E4M3 at D = 64 105
+// and 118. Two row tiles need the registers of two.
 constexpr int q8_ctas_per_sm(int D, int format, int tile_rows) {
   return tile_rows == 16 && (D == 64 || format == HD_Q8_INT8) ? 3 : 2;
 }
@@ -79,7 +73,7 @@ struct Q8Smem {
   static constexpr int KV = kQTile * D;              // bytes of K (or V) of a tile
   static constexpr int STAGES = (RT == 1 ? 2 : 3) * (128 / D);
   static constexpr int RING = kQWarps * STAGES * 2 * KV;
-  static constexpr int Q = 2 * RT * 16 * D;          // the query rows: fp16, or two 8-bit terms
+  static constexpr int Q = RT * 16 * D * 2;          // the query rows in fp16
   static constexpr int FAC = kQWarps * kQTile * 12;  // per warp and key: score factor, log2 vs, 1/vs
   static constexpr int MERGE = kQWarps * RT * 16 * (D + 4) * 4;
   static constexpr int BARS = kQWarps * STAGES * 8;
@@ -102,21 +96,6 @@ __device__ __forceinline__ void mma_f16_16816(float* d, const uint32_t* a, uint3
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(FIRST ? 0.f : d[0]),
         "f"(FIRST ? 0.f : d[1]), "f"(FIRST ? 0.f : d[2]), "f"(FIRST ? 0.f : d[3]));
-}
-
-// d += a b, 16 x 32 by 32 x 8 whole numbers, the sum as the bits of d; FIRST: d
-// starts at the bits of 1.5 * 2^23.
-template <bool FIRST>
-__device__ __forceinline__ void mma_s8_16832(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
-  int c[4], x[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) c[i] = FIRST ? 0x4b400000 : __float_as_int(d[i]);
-  asm volatile(
-      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};\n"
-      : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "r"(c[0]), "r"(c[1]), "r"(c[2]), "r"(c[3]));
-#pragma unroll
-  for (int i = 0; i < 4; ++i) d[i] = __int_as_float(x[i]);
 }
 
 // The codes in bytes (0, 1) and (2, 3) of r (PAIRS), or (0, 2) and (1, 3), as
@@ -385,35 +364,18 @@ __global__ void __launch_bounds__(kQThreads, Q8Smem<D, FMT, RT>::CTAS)
     am = __reduce_max_sync(D == 128 ? 0xffffffffu : 0xffffu << (lane & 16), max(am & 0xffffu, am >> 16));
     const float x[4] = {__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xffff0000u), __uint_as_float(r.y << 16),
                         __uint_as_float(r.y & 0xffff0000u)};
-    float fac;
-    uint32_t u, v;
-    if (FMT == HD_Q8_E4M3) {
-      // A register of an MMA's B operand holds four codes in a row of a key; so of
-      // the 16 k indexes of a step 2t, 2t+1, 2t+8, 2t+9 stand for d = 4t .. 4t+3.
-      const int up = min(14 - (max(static_cast<int>(am >> 7), 1) - 127), 126);
-      const float f = __int_as_float((up + 127) << 23);
-      fac = __int_as_float((127 - up) << 23);
-      u = pack_half(x[0] * f, x[1] * f);
-      v = pack_half(x[2] * f, x[3] * f);
-    } else {
-      const float top = fmaxf(__uint_as_float(am << 16), 1e-30f), f = 32512.f / top;
-      fac = top * (1.f / 32512.f);
-      u = v = 0;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int whole = min(max(__float2int_rn(x[k] * f), -32512), 32512), hi = (whole + 128) >> 8;
-        u |= static_cast<uint32_t>(hi & 0xff) << (8 * k);
-        v |= static_cast<uint32_t>((whole - 256 * hi) & 0xff) << (8 * k);
-      }
-    }
-    if (am >= 0x7f80u) {  // an infinity or NaN: so is every score of the row
-      fac = __int_as_float(0x7fffffff);
-      u = v = 0;
-    }
-    const uint32_t at_u = FMT == HD_Q8_E4M3 ? swz(lr, (d4 >> 2) * 2, D / 8) : swz8<D>(lr, d4 >> 2);
-    const uint32_t at_v = FMT == HD_Q8_E4M3 ? swz(lr, (d4 >> 2) * 2 + 1, D / 8) : at_u + ROWS * D;
-    asm volatile("st.shared.b32 [%0], %1;\n" ::"r"(sQ + at_u + (d4 & 3) * 4), "r"(u) : "memory");
-    asm volatile("st.shared.b32 [%0], %1;\n" ::"r"(sQ + at_v + (d4 & 3) * 4), "r"(v) : "memory");
+    const int up = min(14 - (max(static_cast<int>(am >> 7), 1) - 127), 126);
+    const float f = __int_as_float((up + 127) << 23);
+    // A register of an MMA's B operand holds four codes in a row of a key; so of
+    // the 16 k indexes of a step 2t, 2t+1, 2t+8, 2t+9 stand for d = 4t .. 4t+3.
+    const uint32_t at = sQ + (d4 & 3) * 4;
+    asm volatile("st.shared.b32 [%0], %1;\n" ::"r"(at + swz(lr, (d4 >> 2) * 2, D / 8)), "r"(pack_half(x[0] * f, x[1] * f))
+                 : "memory");
+    asm volatile("st.shared.b32 [%0], %1;\n" ::"r"(at + swz(lr, (d4 >> 2) * 2 + 1, D / 8)),
+                 "r"(pack_half(x[2] * f, x[3] * f))
+                 : "memory");
+    // (an infinity or NaN in the row: so is every score of it)
+    const float fac = am >= 0x7f80u ? __int_as_float(0x7fffffff) : __int_as_float((127 - up) << 23);
     if (d4 == 0) row_fac[lr] = fac;
   }
   __syncthreads();
@@ -465,52 +427,32 @@ __global__ void __launch_bounds__(kQThreads, Q8Smem<D, FMT, RT>::CTAS)
     }
     __syncwarp();
 
-    float s[RT][FMT == HD_Q8_E4M3 ? 1 : 2][kQTile / 8][4];  // (of each term)
+    float s[RT][kQTile / 8][4];
 #pragma unroll
     for (int c4 = 0; c4 < D / 16; c4 += 4) {
       uint32_t r[kQTile / 8][4];
 #pragma unroll
       for (int j = 0; j < kQTile / 8; ++j)  // 8 keys, 64 of d
         ldsm_x4(kb + swz8<D>(j * 8 + (lane & 7), c4 + (lane >> 3)), r[j][0], r[j][1], r[j][2], r[j][3]);
-      if constexpr (FMT == HD_Q8_E4M3) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t qf[RT][4];
+      for (int i = 0; i < 4; ++i) {
+        uint32_t qf[RT][4];
 #pragma unroll
-          for (int rt = 0; rt < RT; ++rt)
-            ldsm_x4(sQ + swz(rt * 16 + (lane & 15), (c4 + i) * 2 + (lane >> 4), D / 8), qf[rt][0], qf[rt][1],
-                    qf[rt][2], qf[rt][3]);
+        for (int rt = 0; rt < RT; ++rt)
+          ldsm_x4(sQ + swz(rt * 16 + (lane & 15), (c4 + i) * 2 + (lane >> 4), D / 8), qf[rt][0], qf[rt][1], qf[rt][2],
+                  qf[rt][3]);
 #pragma unroll
-          for (int j = 0; j < kQTile / 8; ++j) {
-            uint32_t b0, b1;
-            to_half<FMT, true>(r[j][i], b0, b1);
+        for (int j = 0; j < kQTile / 8; ++j) {
+          uint32_t b0, b1;
+          to_half<FMT, true>(r[j][i], b0, b1);
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt) {
-              if (c4 + i == 0)
-                mma_f16_16816<true>(s[rt][0][j], qf[rt], b0, b1);
-              else
-                mma_f16_16816(s[rt][0][j], qf[rt], b0, b1);
-            }
+          for (int rt = 0; rt < RT; ++rt) {
+            if (c4 + i == 0)
+              mma_f16_16816<true>(s[rt][j], qf[rt], b0, b1);
+            else
+              mma_f16_16816(s[rt][j], qf[rt], b0, b1);
           }
         }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; i += 2)
-#pragma unroll
-          for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-            for (int term = 0; term < 2; ++term) {
-              uint32_t qf[4];
-              ldsm_x4(sQ + term * (ROWS * D) + swz8<D>(rt * 16 + (lane & 15), c4 + i + (lane >> 4)), qf[0], qf[1],
-                      qf[2], qf[3]);
-#pragma unroll
-              for (int j = 0; j < kQTile / 8; ++j) {
-                if (c4 + i == 0)
-                  mma_s8_16832<true>(s[rt][term][j], qf, r[j][i], r[j][i + 1]);
-                else
-                  mma_s8_16832<false>(s[rt][term][j], qf, r[j][i], r[j][i + 1]);
-              }
-            }
       }
     }
     const bool all_seen = base + kQTile <= ce && base + kQTile - 1 <= pmin && pmax - base < p.win;
@@ -525,16 +467,10 @@ __global__ void __launch_bounds__(kQThreads, Q8Smem<D, FMT, RT>::CTAS)
         const uint64_t f = lds64(at), lv = lds64(at + kQTile * 4);
 #pragma unroll
         for (int hr = 0; hr < 2; ++hr) {
-          uint64_t dot = pack_f32x2(s[rt][0][j][2 * hr], s[rt][0][j][2 * hr + 1]);
-          if constexpr (FMT == HD_Q8_INT8) {
-            constexpr float kLess = -1.5f * (1 << 23);
-            const uint64_t less = pack_f32x2(kLess, kLess), weigh = pack_f32x2(256.f, 256.f);
-            const uint64_t lo = pack_f32x2(s[rt][1][j][2 * hr], s[rt][1][j][2 * hr + 1]);
-            dot = f32x2_fma(f32x2_add(dot, less), weigh, f32x2_add(lo, less));
-          }
+          const uint64_t dot = pack_f32x2(s[rt][j][2 * hr], s[rt][j][2 * hr + 1]);
           const float2 x = f32x2_parts(f32x2_fma(f32x2_mul(dot, rf2[hr]), f, lv));
-          s[rt][0][j][2 * hr] = x.x;
-          s[rt][0][j][2 * hr + 1] = x.y;
+          s[rt][j][2 * hr] = x.x;
+          s[rt][j][2 * hr + 1] = x.y;
         }
       }
       if (!all_seen) {
@@ -547,14 +483,14 @@ __global__ void __launch_bounds__(kQThreads, Q8Smem<D, FMT, RT>::CTAS)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const int c = base + j * 8 + (lane & 3) * 2 + e;
-              if (!(c < ce && c <= own && own - c < p.win)) s[rt][0][j][2 * hr + e] = -INFINITY;
+              if (!(c < ce && c <= own && own - c < p.win)) s[rt][j][2 * hr + e] = -INFINITY;
             }
         }
       }
 #pragma unroll
       for (int j = 0; j < kQTile / 8; ++j)
 #pragma unroll
-        for (int hr = 0; hr < 2; ++hr) mx[hr] = fmaxf(mx[hr], fmaxf(s[rt][0][j][2 * hr], s[rt][0][j][2 * hr + 1]));
+        for (int hr = 0; hr < 2; ++hr) mx[hr] = fmaxf(mx[hr], fmaxf(s[rt][j][2 * hr], s[rt][j][2 * hr + 1]));
       if (__any_sync(0xffffffffu, mx[0] > m_run[rt][0] + 15.f || mx[1] > m_run[rt][1] + 15.f)) {
 #pragma unroll
         for (int hr = 0; hr < 2; ++hr) {
@@ -582,7 +518,7 @@ __global__ void __launch_bounds__(kQThreads, Q8Smem<D, FMT, RT>::CTAS)
 #pragma unroll
         for (int j = 0; j < kQTile / 8; ++j) {
           const uint64_t iv = lds64(sFac + (2 * kQTile + j * 8 + (lane & 3) * 2) * 4);
-          const float2 x = f32x2_parts(f32x2_add(pack_f32x2(s[rt][0][j][2 * hr], s[rt][0][j][2 * hr + 1]), mu2));
+          const float2 x = f32x2_parts(f32x2_add(pack_f32x2(s[rt][j][2 * hr], s[rt][j][2 * hr + 1]), mu2));
           const float w0 = fast_exp2(x.x), w1 = fast_exp2(x.y);
           l_run[rt][hr] = f32x2_fma(pack_f32x2(w0, w1), iv, l_run[rt][hr]);
           a[rt][j / 2][2 * (j & 1) + hr] = pack_half(w0, w1);
