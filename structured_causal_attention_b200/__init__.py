@@ -29,6 +29,7 @@ torch and call the same C entry points; torch is used for device memory and stre
 """
 from __future__ import annotations
 
+import functools
 from typing import Any, NamedTuple
 
 from ._lib import (  # noqa: F401
@@ -284,22 +285,18 @@ def _cache_q8(cache):
     return B, Tcap, Hkv, D, HD_Q8_E4M3 if k.dtype == torch.float8_e4m3fn else HD_Q8_INT8
 
 
-def _one_device(*ts):
-    """The index of the tensors' one device (``None`` among them is passed over)."""
-    first = ts[0].get_device()
-    for t in ts:
-        if t is not None and t.get_device() != first:
-            raise ValueError("tensors must live on one device")
-    return first
-
-
-def _on(index):
-    """Device ``index`` as the current one: a context."""
-    import contextlib
-
+def _call_on(ts, call, *args):
+    """call(*args) with the one device of the tensors ``ts`` (``None`` among them is passed over) current."""
     import torch
 
-    return contextlib.nullcontext() if index == torch.cuda.current_device() else torch.cuda.device(index)
+    index = ts[0].get_device()
+    for t in ts:
+        if t is not None and t.get_device() != index:
+            raise ValueError("tensors must live on one device")
+    if index == torch.cuda.current_device():
+        return call(*args)
+    with torch.cuda.device(index):
+        return call(*args)
 
 
 def _index_q8(t, B, what):
@@ -325,10 +322,10 @@ def kv_write_q8(k, v, cache, token_offset=None, lengths=None, stream=None):
     _index_q8(token_offset, B, "token_offset")
     _index_q8(lengths, B, "lengths")
     L = k.shape[1] // cache.n
-    with _on(_one_device(cache.k, cache.v, cache.k_scale, cache.v_scale, k, v, token_offset, lengths)):
-        if L:
-            hd_kv_write_q8(k, v, token_offset, lengths, cache.k, cache.v, cache.k_scale, cache.v_scale, B, L,
-                           cache.n, Tcap, Hkv, D, fmt, cache.block_tokens, stream)
+    codes = cache[:4]
+    if L:
+        _call_on((*codes, k, v, token_offset, lengths), hd_kv_write_q8, k, v, token_offset, lengths, *codes, B, L,
+                 cache.n, Tcap, Hkv, D, fmt, cache.block_tokens, stream)
 
 
 def kv_read_q8(cache, L, token_offset=None, lengths=None, out=None, stream=None):
@@ -346,10 +343,10 @@ def kv_read_q8(cache, L, token_offset=None, lengths=None, out=None, stream=None)
     _need_cuda(k, v)
     if k.dtype != torch.bfloat16 or v.dtype != torch.bfloat16 or k.shape != shape or v.shape != shape:
         raise ValueError(f"out must be two bfloat16 tensors {list(shape)}")
-    with _on(_one_device(cache.k, cache.v, cache.k_scale, cache.v_scale, token_offset, lengths, k, v)):
-        if L:
-            hd_kv_read_q8(cache.k, cache.v, cache.k_scale, cache.v_scale, token_offset, lengths, k, v, B, L,
-                          cache.n, Tcap, Hkv, D, fmt, cache.block_tokens, stream)
+    codes = cache[:4]
+    if L:
+        _call_on((*codes, token_offset, lengths, k, v), hd_kv_read_q8, *codes, token_offset, lengths, k, v, B, L,
+                 cache.n, Tcap, Hkv, D, fmt, cache.block_tokens, stream)
     return k, v
 
 
@@ -368,16 +365,24 @@ def _decode_q8(q, cache, seqlen, mode, W, scale, stream, workspace, final):
     Hq = q.shape[2]
     if scale is None:
         scale = D ** -0.5
-    with _on(_one_device(q, cache.k, cache.v, cache.k_scale, cache.v_scale, seqlen, workspace)):
-        out = torch.empty_like(q)
-        lse = q.new_empty((B, Hq, nq), dtype=torch.float32)
-        if workspace is None:
-            size = hd_decode_final_q8_workspace_bytes if final else hd_decode_q8_workspace_bytes
-            workspace = q.new_empty(size(B, n, Tcap, Hq, Hkv, D), dtype=torch.uint8)
-        call = hd_decode_attn_final_q8 if final else hd_decode_attn_q8
-        call(q, cache.k, cache.v, cache.k_scale, cache.v_scale, seqlen, out, lse, B, n, Tcap, Hq, Hkv, D, fmt,
-             cache.block_tokens, mode, W, scale, workspace, workspace.numel() * workspace.element_size(), stream)
+    out = torch.empty_like(q)
+    lse = q.new_empty((B, Hq, nq), dtype=torch.float32)
+    if workspace is None:
+        workspace = q.new_empty(_decode_q8_bytes(q.get_device(), final, B, n, Tcap, Hq, Hkv, D), dtype=torch.uint8)
+    codes = cache[:4]
+    _call_on((q, *codes, seqlen, workspace), hd_decode_attn_final_q8 if final else hd_decode_attn_q8, q, *codes, seqlen,
+             out, lse, B, n, Tcap, Hq, Hkv, D, fmt, cache.block_tokens, mode, W, scale, workspace,
+             workspace.numel() * workspace.element_size(), stream)
     return out, lse
+
+
+@functools.lru_cache(maxsize=256)
+def _decode_q8_bytes(index, final, *sizes):
+    """The workspace's size on device ``index`` (it goes by the sizes and the number of its SMs)."""
+    import torch
+
+    with torch.cuda.device(index):
+        return (hd_decode_final_q8_workspace_bytes if final else hd_decode_q8_workspace_bytes)(*sizes)
 
 
 def decode_attn_q8(q, cache, seqlen, mode, W=0, scale=None, stream=None, workspace=None):
