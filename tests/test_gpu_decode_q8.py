@@ -277,3 +277,44 @@ def test_decode_workload(mode, fmt, final):
         at = slice(b, b + 1)
         one = cache._replace(**{x: getattr(cache, x)[at] for x in ("k", "v", "k_scale", "v_scale")})
         check_attention(out[at], lse[at], q[at], on_host(one), n, cache.block_tokens, fmt, seqlen[at], mode, 1024, w["scale"], final)
+
+
+def test_other_stream_by_argument_and_shared_workspace_in_order():
+    """The stream argument, and one workspace for calls that follow one another on a stream."""
+    need_gpu()
+    B, n, T, Hq, Hkv, D = 2, 4, 1500, 16, 4, 64
+    seqlen = _lengths(B, T, 3, False).cuda()
+    cache = _filled(B, T, n, Hkv, D, "int8", 16, seqlen.cpu(), 4)
+    q = [syn.normal_bf16((B, n, Hq, D), 5 + i).cuda() for i in range(3)]
+    alone = [hd.decode_attn_q8(x, cache, seqlen, hd.CROSS_FULL) for x in q]
+    ws = torch.empty(hd.hd_decode_q8_workspace_bytes(B, n, T, Hq, Hkv, D), dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    got = [hd.decode_attn_q8(x, cache, seqlen, hd.CROSS_FULL, stream=s, workspace=ws) for x in q]
+    s.synchronize()
+    for a, b in zip(alone, got):
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_cache_past_32_bits(fmt):
+    """Codes beyond 2^32 elements: the second sequence's keys lie there."""
+    need_gpu()
+    B, n, Hq, Hkv, D, bt, Tcap = 2, 8, 16, 16, 128, 16, 300_000
+    cache = hd.kv_cache_q8(B, Tcap, n, Hkv, D, torch.int8 if fmt == "int8" else torch.float8_e4m3fn, bt)
+    T = 40
+    k, v = rows((B, T * n, Hkv, D), 1, n), rows((B, T * n, Hkv, D), 2, n)
+    hd.kv_write_q8(k.cuda(), v.cuda(), cache)
+    seqlen = torch.tensor([T, T], dtype=torch.int32)
+    q = syn.normal_bf16((B, n, Hq, D), 3)
+    out, lse = _attend(q, cache, seqlen, hd.CROSS_FULL, 0, 0.1, False)
+    short = cache._replace(**{x: getattr(cache, x)[:, :T * n].contiguous() for x in ("k", "v")},
+                           **{x: getattr(cache, x)[:, :, :-(-T // bt)].contiguous() for x in ("k_scale", "v_scale")})
+    check_attention(out, lse, q, on_host(short), n, bt, fmt, seqlen, hd.CROSS_FULL, 0, 0.1, False)
+    # and its last keys: the last stream's window of 16 tokens is exactly the last 16 tokens' rows
+    seqlen = torch.tensor([T, Tcap], dtype=torch.int32)
+    hd.kv_write_q8(k[:, :16 * n].contiguous().cuda(), v[:, :16 * n].contiguous().cuda(), cache,
+                   torch.tensor([0, Tcap - 16], dtype=torch.int32, device="cuda"))
+    out, lse = _attend(q[:, -1:], cache, seqlen, hd.CROSS_WINDOW, 16, 0.1, True)
+    tail = hd.KVCacheQ8(cache.k[1:, -16 * n:], cache.v[1:, -16 * n:], cache.k_scale[1:, :, -1:], cache.v_scale[1:, :, -1:], n, bt)
+    check_attention(out[1:], lse[1:], q[1:, -1:], on_host(tail), n, bt, fmt, torch.tensor([16]), hd.CROSS_FULL, 0, 0.1, True)
