@@ -245,7 +245,7 @@ def lm_head_ce_bwd(x, w, labels, lse, n, grad_scale=1.0, stream=None, workspace=
 class KVCacheQ8(NamedTuple):
     """An 8-bit KV cache: codes [B, Tcap*n, Hkv, D], float8_e4m3fn or int8 (the format), and fp32 scales
     [B, Hkv, ceil(Tcap / block_tokens), n]. ``kv_cache_q8`` makes one; any four tensors of these
-    shapes do."""
+    shapes do, as what they hold is written by ``kv_write_q8``."""
 
     k: Any
     v: Any

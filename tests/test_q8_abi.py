@@ -22,6 +22,7 @@ BAD_ROWS = [
     (dict(ks=FAKE + 4), 1), (dict(vs=FAKE + 8), 1), (dict(B=0), 1), (dict(L=0), 1), (dict(n=0), 1), (dict(Tcap=0), 1),
     (dict(Hkv=0), 1), (dict(D=0), 1), (dict(fmt=2), 1), (dict(fmt=-1), 1), (dict(bt=0), 1), (dict(bt=-4), 1),
     (dict(bt=1025), 2), (dict(D=96), 2), (dict(D=256), 2), (dict(Tcap=1 << 27), 2), (dict(L=1 << 27), 2),
+    (dict(L=1 << 24, Hkv=8), 2),  # more than 2^31 chunks of 8 elements a sequence
 ]
 
 
