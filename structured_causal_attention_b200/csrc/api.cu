@@ -288,7 +288,7 @@ size_t decode_q8_problem(DecodeQ8Params& p, int mode, int W_tokens, int final_on
   p.tile_rows = decode_q8_tile_rows(p.rows);
   p.mt = (p.rows + p.tile_rows - 1) / p.tile_rows;
   const long long problems = static_cast<long long>(p.B) * p.groups;
-  decode_q8_plan(problems, keys, p.D, p.format, p.tile_rows, static_cast<long long>(p.Hkv) * p.mt, sm_count(), &p.ctas, &p.least,
+  decode_q8_plan(problems, keys, p.tile_rows, static_cast<long long>(p.Hkv) * p.mt, sm_count(), &p.ctas, &p.least,
                  &p.whole);
   p.slots = static_cast<int>(problems) + p.ctas;
   const size_t prow = p.whole ? 1 : static_cast<size_t>(p.mt) * p.Hkv * p.tile_rows * p.slots;  // (never empty)
@@ -296,24 +296,22 @@ size_t decode_q8_problem(DecodeQ8Params& p, int mode, int W_tokens, int final_on
   return align256(prow * static_cast<size_t>(p.D) * 4) + align256(prow * 2 * 4);
 }
 
-// The most that any mode, window and format needs. (A window's pieces are no more than
+// The most that any mode and window needs. (A window's pieces are no more than
 // those of the whole cache.)
 size_t decode_q8_workspace(int B, int n, int Tcap, int Hq, int Hkv, int D, int final_only) {
   if (B < 1 || n < 1 || Tcap < 1 || Hq < 1 || Hkv < 1 || D < 1 || Hq % Hkv) return 0;
   size_t most = 0;
-  for (int mode = HD_INTRA; mode <= HD_CROSS_FULL; ++mode)
-    for (int format = HD_Q8_E4M3; format <= HD_Q8_INT8; ++format) {
-      DecodeQ8Params p = {};
-      p.B = B;
-      p.n = n;
-      p.Tcap = Tcap;
-      p.Hq = Hq;
-      p.Hkv = Hkv;
-      p.D = D;
-      p.format = format;
-      const size_t need = decode_q8_problem(p, mode, 1, final_only);
-      if (need > most) most = need;
-    }
+  for (int mode = HD_INTRA; mode <= HD_CROSS_FULL; ++mode) {
+    DecodeQ8Params p = {};
+    p.B = B;
+    p.n = n;
+    p.Tcap = Tcap;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.D = D;
+    const size_t need = decode_q8_problem(p, mode, 1, final_only);
+    if (need > most) most = need;
+  }
   return most;
 }
 

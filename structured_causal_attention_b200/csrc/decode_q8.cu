@@ -57,19 +57,15 @@ constexpr int kQTile = 32;  // keys of a warp's tile
 static_assert(kQWarps * kQTile == kQ8Round, "a round");
 constexpr float kLn2 = 0.69314718055994530942f;
 
-// CTAs of an SM. Three hide more latency, but for E4M3 at D = 128, whose copies in
-// flight are then so many that HBM delivers less: 8 sequences of 16385 tokens took
-// 195 us with three and 176 with two (64 sequences, at the power cap's lower
-// clock: 1390 and 1520); INT8, with more to compute, 186 and 196 (1550 and 1740), E4M3 at D = 64 105
-// and 118. Two row tiles need the registers of two.
-constexpr int q8_ctas_per_sm(int D, int format, int tile_rows) {
-  return tile_rows == 16 && (D == 64 || format == HD_Q8_INT8) ? 3 : 2;
-}
+// CTAs of an SM. Three hide more latency than two: 64 sequences of 16385 tokens in
+// INT8 took 1574 us with three and 1650 with two, 8 in E4M3 191 and 196, at D = 64
+// 105 and 118. Two row tiles need the registers of two.
+constexpr int q8_ctas_per_sm(int tile_rows) { return tile_rows == 16 ? 3 : 2; }
 
 // RT row tiles of 16 a CTA: the codes are converted once for all of them.
-template <int D, int FMT, int RT>
+template <int D, int RT>
 struct Q8Smem {
-  static constexpr int CTAS = q8_ctas_per_sm(D, FMT, RT * 16);
+  static constexpr int CTAS = q8_ctas_per_sm(RT * 16);
   static constexpr int KV = kQTile * D;              // bytes of K (or V) of a tile
   static constexpr int STAGES = (RT == 1 ? 2 : 3) * (128 / D);
   static constexpr int RING = kQWarps * STAGES * 2 * KV;
@@ -240,10 +236,10 @@ __device__ __forceinline__ Q8Line q8_line(const DecodeQ8Params& p, int lane) {
 }
 
 template <int D, int FMT, int RT>
-__global__ void __launch_bounds__(kQThreads, Q8Smem<D, FMT, RT>::CTAS)
+__global__ void __launch_bounds__(kQThreads, Q8Smem<D, RT>::CTAS)
     decode_q8_split_kernel(const DecodeQ8Params p, const __grid_constant__ CUtensorMap tmK,
                            const __grid_constant__ CUtensorMap tmV) {
-  using SM = Q8Smem<D, FMT, RT>;
+  using SM = Q8Smem<D, RT>;
   constexpr int S = SM::STAGES, ROWS = 16 * RT;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -758,7 +754,7 @@ cudaError_t launch_decode_q8_d(const DecodeQ8Params& p, cudaStream_t stream) {
   const long long R = intra ? p.Tcap : static_cast<long long>(p.Tcap) * p.n;
   CUtensorMap mk, mv;
   if (!make_map<D>(&mk, p.kc, J, R, p.B) || !make_map<D>(&mv, p.vc, J, R, p.B)) return cudaErrorInvalidValue;
-  const int smem = Q8Smem<D, FMT, RT>::TOTAL;
+  const int smem = Q8Smem<D, RT>::TOTAL;
   cudaError_t e = cudaFuncSetAttribute(decode_q8_split_kernel<D, FMT, RT>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
@@ -793,10 +789,10 @@ int decode_q8_tile_rows(int rows) { return rows <= 16 ? 16 : 32; }
 // least, and whether each CTA takes one problem whole instead of a piece: where
 // none has more than kWhole rounds, dividing one and joining its parts takes
 // longer than it saves, and the second kernel is left out.
-void decode_q8_plan(long long problems, long long most_keys, int D, int format, int tile_rows, long long lines, int sms, int* ctas,
+void decode_q8_plan(long long problems, long long most_keys, int tile_rows, long long lines, int sms, int* ctas,
                     int* least, int* whole) {
   constexpr int kWhole = 8;
-  const long long slots = sms * q8_ctas_per_sm(D, format, tile_rows) / lines;
+  const long long slots = sms * q8_ctas_per_sm(tile_rows) / lines;
   *whole = most_keys <= kWhole * kQ8Round;
   *least = 2;
   *ctas = static_cast<int>(*whole ? problems : (slots > 1 ? slots : 1));
