@@ -60,20 +60,21 @@ constexpr float kLn2 = 0.69314718055994530942f;
 // CTAs of an SM. Three hide more latency than two: 64 sequences of 16385 tokens in
 // INT8 took 1574 us with three and 1650 with two, 8 in E4M3 191 and 196, at D = 64
 // 105 and 118. Two row tiles need the registers of two.
-constexpr int q8_ctas_per_sm(int tile_rows) { return tile_rows == 16 ? 3 : 2; }
+constexpr int q8_ctas_per_sm(int tile_rows) { return tile_rows <= 16 ? 3 : 2; }
 
-// RT row tiles of 16 a CTA: the codes are converted once for all of them.
-template <int D, int RT>
+// TR query rows a CTA: 8, 16 or 32 (two tiles of 16, the codes converted once for
+// both).
+template <int D, int TR>
 struct Q8Smem {
-  static constexpr int CTAS = q8_ctas_per_sm(RT * 16);
+  static constexpr int CTAS = q8_ctas_per_sm(TR);
   static constexpr int KV = kQTile * D;              // bytes of K (or V) of a tile
-  static constexpr int STAGES = (RT == 1 ? 2 : 3) * (128 / D);
+  static constexpr int STAGES = (TR <= 16 ? 2 : 3) * (128 / D);
   static constexpr int RING = kQWarps * STAGES * 2 * KV;
-  static constexpr int Q = RT * 16 * D * 2;          // the query rows in fp16
+  static constexpr int Q = TR * D * 2;          // the query rows in fp16
   static constexpr int FAC = kQWarps * kQTile * 12;  // per warp and key: score factor, log2 vs, 1/vs
-  static constexpr int MERGE = kQWarps * RT * 16 * (D + 4) * 4;
+  static constexpr int MERGE = kQWarps * TR * (D + 4) * 4;
   static constexpr int BARS = kQWarps * STAGES * 8;
-  static constexpr int TOTAL = RING + Q + FAC + BARS + RT * 64 + 16 + 1024;  // and the alignment of the ring
+  static constexpr int TOTAL = RING + Q + FAC + BARS + TR * 4 + 16 + 1024;  // and the alignment of the ring
   static_assert(MERGE <= RING, "merge buffer");
 };
 
@@ -147,6 +148,17 @@ __device__ __forceinline__ float ldg_here(const float* at) {
   float x;
   asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(x) : "l"(at));
   return x;
+}
+__device__ __forceinline__ float lds32(uint32_t addr) {
+  float r;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(r) : "r"(addr));
+  return r;
+}
+// An 8 x 8 tile of fp16 pairs across the warp, transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
 }
 __device__ __forceinline__ uint64_t lds64(uint32_t addr) {
   uint64_t r;
@@ -235,12 +247,335 @@ __device__ __forceinline__ Q8Line q8_line(const DecodeQ8Params& p, int lane) {
   return {total, max((total + p.ctas - 1) / p.ctas, p.least)};
 }
 
+// What the queries see of a warp's tile: keys base .. base + 31, those from `end` on
+// behind the piece; all: every row sees every one of them.
+struct Q8Seen {
+  bool all;
+  int base, end, win;
+  int t0, g, row0, last;  // own key of row r: t0 + min(row0 + r, last) / g (g = 0: t0)
+  __device__ __forceinline__ int own(int r) const { return g ? t0 + min(row0 + r, last) / g : t0; }
+};
+
+// The state of a warp with 16 RT query rows: rows are the M of its MMAs.
 template <int D, int FMT, int RT>
-__global__ void __launch_bounds__(kQThreads, Q8Smem<D, RT>::CTAS)
+struct Q8Rows {
+  static constexpr int ROWS = 16 * RT;
+  float rf[RT][2];  // the rows' factors: rows lane/4, lane/4 + 8 of each tile
+  // o[rt][c][h]: d = c*16 + 4t + h and + 2 + h (h = 0, 1) of those rows
+  float o[RT][D / 16][2][4];
+  float m_run[RT][2];
+  uint64_t l_run[RT][2];  // two partial sums a row
+
+  __device__ __forceinline__ void start(uint32_t, const float* row_fac, int lane) {
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+#pragma unroll
+      for (int hr = 0; hr < 2; ++hr) rf[rt][hr] = row_fac[rt * 16 + (lane >> 2) + hr * 8];
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[rt][c][0][e] = o[rt][c][1][e] = 0.f;
+      m_run[rt][0] = m_run[rt][1] = -INFINITY;
+      l_run[rt][0] = l_run[rt][1] = 0;
+    }
+  }
+
+  // The tile with its K and V at kb and vb, the keys' factors at sFac.
+  __device__ __forceinline__ void tile(uint32_t sQ, uint32_t kb, uint32_t vb, uint32_t sFac, const Q8Seen& seen,
+                                       int lane) {
+    float s[RT][kQTile / 8][4];
+#pragma unroll
+    for (int c4 = 0; c4 < D / 16; c4 += 4) {
+      uint32_t r[kQTile / 8][4];
+#pragma unroll
+      for (int j = 0; j < kQTile / 8; ++j)  // 8 keys, 64 of d
+        ldsm_x4(kb + swz8<D>(j * 8 + (lane & 7), c4 + (lane >> 3)), r[j][0], r[j][1], r[j][2], r[j][3]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t qf[RT][4];
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+          ldsm_x4(sQ + swz(rt * 16 + (lane & 15), (c4 + i) * 2 + (lane >> 4), D / 8), qf[rt][0], qf[rt][1], qf[rt][2],
+                  qf[rt][3]);
+#pragma unroll
+        for (int j = 0; j < kQTile / 8; ++j) {
+          uint32_t b0, b1;
+          to_half<FMT, true>(r[j][i], b0, b1);
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt) {
+            if (c4 + i == 0)
+              mma_f16_16816<true>(s[rt][j], qf[rt], b0, b1);
+            else
+              mma_f16_16816(s[rt][j], qf[rt], b0, b1);
+          }
+        }
+      }
+    }
+    uint32_t a[RT][kQTile / 16][4];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      float mx[2] = {-INFINITY, -INFINITY};
+      const uint64_t rf2[2] = {pack_f32x2(rf[rt][0], rf[rt][0]), pack_f32x2(rf[rt][1], rf[rt][1])};
+#pragma unroll
+      for (int j = 0; j < kQTile / 8; ++j) {
+        const uint32_t at = sFac + (j * 8 + (lane & 3) * 2) * 4;
+        const uint64_t f = lds64(at), lv = lds64(at + kQTile * 4);
+#pragma unroll
+        for (int hr = 0; hr < 2; ++hr) {
+          const uint64_t dot = pack_f32x2(s[rt][j][2 * hr], s[rt][j][2 * hr + 1]);
+          const float2 x = f32x2_parts(f32x2_fma(f32x2_mul(dot, rf2[hr]), f, lv));
+          s[rt][j][2 * hr] = x.x;
+          s[rt][j][2 * hr + 1] = x.y;
+        }
+      }
+      if (!seen.all) {
+#pragma unroll
+        for (int hr = 0; hr < 2; ++hr) {
+          const int own = seen.own(rt * 16 + (lane >> 2) + hr * 8);
+#pragma unroll
+          for (int j = 0; j < kQTile / 8; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int c = seen.base + j * 8 + (lane & 3) * 2 + e;
+              if (!(c < seen.end && c <= own && own - c < seen.win)) s[rt][j][2 * hr + e] = -INFINITY;
+            }
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kQTile / 8; ++j)
+#pragma unroll
+        for (int hr = 0; hr < 2; ++hr) mx[hr] = fmaxf(mx[hr], fmaxf(s[rt][j][2 * hr], s[rt][j][2 * hr + 1]));
+      if (__any_sync(0xffffffffu, mx[0] > m_run[rt][0] + 15.f || mx[1] > m_run[rt][1] + 15.f)) {
+#pragma unroll
+        for (int hr = 0; hr < 2; ++hr) {
+          float m = fmaxf(mx[hr], __shfl_xor_sync(0xffffffffu, mx[hr], 1));
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+          if (m > m_run[rt][hr] + 15.f) {
+            const float alpha = fast_exp2(m_run[rt][hr] - (m - 13.f));
+            m_run[rt][hr] = m - 13.f;
+            const float2 l = f32x2_parts(l_run[rt][hr]);
+            l_run[rt][hr] = pack_f32x2(l.x * alpha, l.y * alpha);
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                o[rt][c][h][2 * hr] *= alpha;
+                o[rt][c][h][2 * hr + 1] *= alpha;
+              }
+          }
+        }
+      }
+#pragma unroll
+      for (int hr = 0; hr < 2; ++hr) {
+        const float mu = m_run[rt][hr] == -INFINITY ? 0.f : -m_run[rt][hr];
+        const uint64_t mu2 = pack_f32x2(mu, mu);
+#pragma unroll
+        for (int j = 0; j < kQTile / 8; ++j) {
+          const uint64_t iv = lds64(sFac + (2 * kQTile + j * 8 + (lane & 3) * 2) * 4);
+          const float2 x = f32x2_parts(f32x2_add(pack_f32x2(s[rt][j][2 * hr], s[rt][j][2 * hr + 1]), mu2));
+          const float w0 = fast_exp2(x.x), w1 = fast_exp2(x.y);
+          l_run[rt][hr] = f32x2_fma(pack_f32x2(w0, w1), iv, l_run[rt][hr]);
+          a[rt][j / 2][2 * (j & 1) + hr] = pack_half(w0, w1);
+        }
+      }
+    }
+#pragma unroll
+    for (int k16 = 0; k16 < kQTile / 16; ++k16)
+#pragma unroll
+      for (int c = 0; c < D / 16; c += 2) {  // 16 keys, 32 of d
+        uint32_t r[4];
+        ldsm_x4_t(vb + swz8<D>(k16 * 16 + (lane & 15), c + (lane >> 4)), r[0], r[1], r[2], r[3]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          uint32_t e0, o0, e1, o1;
+          to_half<FMT, false>(r[2 * i], e0, o0);
+          to_half<FMT, false>(r[2 * i + 1], e1, o1);
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt) {
+            mma_f16_16816(o[rt][c + i][0], a[rt][k16], e0, e1);
+            mma_f16_16816(o[rt][c + i][1], a[rt][k16], o0, o1);
+          }
+        }
+      }
+  }
+
+  // This warp's [ROWS][D+4]: values, reference, sum.
+  __device__ __forceinline__ void store(float* to, int lane) const {
+    constexpr int RS = D + 4;
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+      for (int hr = 0; hr < 2; ++hr) {
+        const float2 lp = f32x2_parts(l_run[rt][hr]);
+        float l = lp.x + lp.y;
+        l += __shfl_xor_sync(0xffffffffu, l, 1);
+        l += __shfl_xor_sync(0xffffffffu, l, 2);
+        float* rowp = to + (rt * 16 + (lane >> 2) + hr * 8) * RS;
+        if ((lane & 3) == 0) {
+          rowp[D] = m_run[rt][hr];
+          rowp[D + 1] = l;
+        }
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c)
+          *reinterpret_cast<float4*>(rowp + c * 16 + (lane & 3) * 4) =
+              make_float4(o[rt][c][0][2 * hr], o[rt][c][1][2 * hr], o[rt][c][0][2 * hr + 1], o[rt][c][1][2 * hr + 1]);
+      }
+  }
+};
+
+// The state of a warp with 8 query rows: keys are the M of its MMAs, the rows their
+// N, so that none of M = 16 is padding. S^T = K Q^T leaves a lane with the rows 2t,
+// 2t+1 of keys; transposed 8 x 8 by 8 x 8 the weights are the operand of
+// O^T = V^T P^T.
+template <int D, int FMT>
+struct Q8Rows8 {
+  static constexpr int ROWS = 8;
+  uint64_t rf;            // the factors of rows 2t, 2t+1
+  uint32_t qb[D / 16][2];
+  float o[D / 16][4];     // d = c*16 + 2g of rows 2t, 2t+1; d + 1 of them (g = lane/4)
+  float m_run[2];
+  uint64_t l_run;         // of rows 2t, 2t+1, over this lane's keys
+
+  __device__ __forceinline__ void start(uint32_t sQ, const float* row_fac, int lane) {
+    rf = pack_f32x2(row_fac[(lane & 3) * 2], row_fac[(lane & 3) * 2 + 1]);
+#pragma unroll
+    for (int c = 0; c < D / 16; c += 2)
+      ldsm_x4(sQ + swz(lane & 7, c * 2 + (lane >> 3), D / 8), qb[c][0], qb[c][1], qb[c + 1][0], qb[c + 1][1]);
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) o[c][0] = o[c][1] = o[c][2] = o[c][3] = 0.f;
+    m_run[0] = m_run[1] = -INFINITY;
+    l_run = 0;
+  }
+
+  __device__ __forceinline__ void tile(uint32_t, uint32_t kb, uint32_t vb, uint32_t sFac, const Q8Seen& seen, int lane) {
+    const int g = lane >> 2;
+    float s[kQTile / 16][4];  // of key 16i + g: rows 2t, 2t+1; of key 16i + g + 8: the same
+#pragma unroll
+    for (int c = 0; c < D / 16; c += 2)
+#pragma unroll
+      for (int i = 0; i < kQTile / 16; ++i) {  // 16 keys, 32 of d
+        uint32_t r[4], a[4];
+        ldsm_x4(kb + swz8<D>(i * 16 + (lane & 15), c + (lane >> 4)), r[0], r[1], r[2], r[3]);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          to_half<FMT, true>(r[2 * j], a[0], a[2]);
+          to_half<FMT, true>(r[2 * j + 1], a[1], a[3]);
+          if (c + j == 0)
+            mma_f16_16816<true>(s[i], a, qb[c + j][0], qb[c + j][1]);
+          else
+            mma_f16_16816(s[i], a, qb[c + j][0], qb[c + j][1]);
+        }
+      }
+    float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+    for (int i = 0; i < kQTile / 16; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t at = sFac + (i * 16 + h * 8 + g) * 4;
+        const float f = lds32(at), lv = lds32(at + kQTile * 4);
+        const float2 x = f32x2_parts(
+            f32x2_fma(f32x2_mul(pack_f32x2(s[i][2 * h], s[i][2 * h + 1]), rf), pack_f32x2(f, f), pack_f32x2(lv, lv)));
+        s[i][2 * h] = x.x;
+        s[i][2 * h + 1] = x.y;
+      }
+    if (!seen.all) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int own = seen.own((lane & 3) * 2 + e);
+#pragma unroll
+        for (int i = 0; i < kQTile / 16; ++i)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int c = seen.base + i * 16 + h * 8 + g;
+            if (!(c < seen.end && c <= own && own - c < seen.win)) s[i][2 * h + e] = -INFINITY;
+          }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kQTile / 16; ++i)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) mx[e] = fmaxf(mx[e], fmaxf(s[i][e], s[i][2 + e]));
+    if (__any_sync(0xffffffffu, mx[0] > m_run[0] + 15.f || mx[1] > m_run[1] + 15.f)) {
+      float alpha[2] = {1.f, 1.f};
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float m = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 4));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+        if (m > m_run[e] + 15.f) {
+          alpha[e] = fast_exp2(m_run[e] - (m - 13.f));
+          m_run[e] = m - 13.f;
+        }
+      }
+      l_run = f32x2_mul(l_run, pack_f32x2(alpha[0], alpha[1]));
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[c][e] *= alpha[e & 1];
+    }
+    const uint64_t mu = pack_f32x2(m_run[0] == -INFINITY ? 0.f : -m_run[0], m_run[1] == -INFINITY ? 0.f : -m_run[1]);
+#pragma unroll
+    for (int i = 0; i < kQTile / 16; ++i) {
+      uint32_t b[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float iv = lds32(sFac + (2 * kQTile + i * 16 + h * 8 + g) * 4);
+        const float2 x = f32x2_parts(f32x2_add(pack_f32x2(s[i][2 * h], s[i][2 * h + 1]), mu));
+        const float w0 = fast_exp2(x.x), w1 = fast_exp2(x.y);
+        l_run = f32x2_fma(pack_f32x2(w0, w1), pack_f32x2(iv, iv), l_run);
+        b[h] = transpose8(pack_half(w0, w1));
+      }
+#pragma unroll
+      for (int c = 0; c < D / 16; c += 2) {  // 16 keys, 32 of d
+        uint32_t r[4], a[4];
+        ldsm_x4_t(vb + swz8<D>(i * 16 + (lane & 15), c + (lane >> 4)), r[0], r[1], r[2], r[3]);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {  // (row g of M is d = 2g, row g + 8 d = 2g + 1)
+          to_half<FMT, false>(r[2 * j], a[0], a[1]);
+          to_half<FMT, false>(r[2 * j + 1], a[2], a[3]);
+          mma_f16_16816(o[c + j], a, b[0], b[1]);
+        }
+      }
+    }
+  }
+
+  __device__ __forceinline__ void store(float* to, int lane) const {
+    constexpr int RS = D + 4;
+    const float2 lp = f32x2_parts(l_run);
+    const float part[2] = {lp.x, lp.y};
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float l = part[e];
+      l += __shfl_xor_sync(0xffffffffu, l, 4);
+      l += __shfl_xor_sync(0xffffffffu, l, 8);
+      l += __shfl_xor_sync(0xffffffffu, l, 16);
+      float* rowp = to + ((lane & 3) * 2 + e) * RS;
+      if (lane < 4) {
+        rowp[D] = m_run[e];
+        rowp[D + 1] = l;
+      }
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c)
+        *reinterpret_cast<float2*>(rowp + c * 16 + (lane >> 2) * 2) = make_float2(o[c][e], o[c][2 + e]);
+    }
+  }
+};
+
+template <int D, int FMT, int TR>
+struct Q8RowsOf {
+  using type = Q8Rows<D, FMT, TR / 16>;
+};
+template <int D, int FMT>
+struct Q8RowsOf<D, FMT, 8> {
+  using type = Q8Rows8<D, FMT>;
+};
+
+template <int D, int FMT, int TR>
+__global__ void __launch_bounds__(kQThreads, Q8Smem<D, TR>::CTAS)
     decode_q8_split_kernel(const DecodeQ8Params p, const __grid_constant__ CUtensorMap tmK,
                            const __grid_constant__ CUtensorMap tmV) {
-  using SM = Q8Smem<D, RT>;
-  constexpr int S = SM::STAGES, ROWS = 16 * RT;
+  using SM = Q8Smem<D, TR>;
+  constexpr int S = SM::STAGES, ROWS = TR;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t sRing = smem_u32(smem), sQ = sRing + SM::RING;
@@ -375,25 +710,8 @@ __global__ void __launch_bounds__(kQThreads, Q8Smem<D, RT>::CTAS)
     if (d4 == 0) row_fac[lr] = fac;
   }
   __syncthreads();
-  float rf[RT][2];
-#pragma unroll
-  for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-    for (int hr = 0; hr < 2; ++hr) rf[rt][hr] = row_fac[rt * 16 + (lane >> 2) + hr * 8];
-
-  // o[rt][c][h]: d = c*16 + 4t + h and + 2 + h (h = 0, 1) of rows lane/4, lane/4 + 8
-  float o[RT][D / 16][2][4];
-  float m_run[RT][2];
-  uint64_t l_run[RT][2];  // two partial sums a row
-#pragma unroll
-  for (int rt = 0; rt < RT; ++rt) {
-#pragma unroll
-    for (int c = 0; c < D / 16; ++c)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[rt][c][0][e] = o[rt][c][1][e] = 0.f;
-    m_run[rt][0] = m_run[rt][1] = -INFINITY;
-    l_run[rt][0] = l_run[rt][1] = 0;
-  }
+  typename Q8RowsOf<D, FMT, TR>::type rows;
+  rows.start(sQ, row_fac, lane);
   const uint32_t sFac = sQ + SM::Q + warp * (kQTile * 12);
   float* fac = reinterpret_cast<float*>(smem + SM::RING + SM::Q) + warp * (kQTile * 3);
   int done = 0;  // tiles whose copies have arrived
@@ -423,122 +741,9 @@ __global__ void __launch_bounds__(kQThreads, Q8Smem<D, RT>::CTAS)
     }
     __syncwarp();
 
-    float s[RT][kQTile / 8][4];
-#pragma unroll
-    for (int c4 = 0; c4 < D / 16; c4 += 4) {
-      uint32_t r[kQTile / 8][4];
-#pragma unroll
-      for (int j = 0; j < kQTile / 8; ++j)  // 8 keys, 64 of d
-        ldsm_x4(kb + swz8<D>(j * 8 + (lane & 7), c4 + (lane >> 3)), r[j][0], r[j][1], r[j][2], r[j][3]);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t qf[RT][4];
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
-          ldsm_x4(sQ + swz(rt * 16 + (lane & 15), (c4 + i) * 2 + (lane >> 4), D / 8), qf[rt][0], qf[rt][1], qf[rt][2],
-                  qf[rt][3]);
-#pragma unroll
-        for (int j = 0; j < kQTile / 8; ++j) {
-          uint32_t b0, b1;
-          to_half<FMT, true>(r[j][i], b0, b1);
-#pragma unroll
-          for (int rt = 0; rt < RT; ++rt) {
-            if (c4 + i == 0)
-              mma_f16_16816<true>(s[rt][j], qf[rt], b0, b1);
-            else
-              mma_f16_16816(s[rt][j], qf[rt], b0, b1);
-          }
-        }
-      }
-    }
-    const bool all_seen = base + kQTile <= ce && base + kQTile - 1 <= pmin && pmax - base < p.win;
-    uint32_t a[RT][kQTile / 16][4];
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-      float mx[2] = {-INFINITY, -INFINITY};
-      const uint64_t rf2[2] = {pack_f32x2(rf[rt][0], rf[rt][0]), pack_f32x2(rf[rt][1], rf[rt][1])};
-#pragma unroll
-      for (int j = 0; j < kQTile / 8; ++j) {
-        const uint32_t at = sFac + (j * 8 + (lane & 3) * 2) * 4;
-        const uint64_t f = lds64(at), lv = lds64(at + kQTile * 4);
-#pragma unroll
-        for (int hr = 0; hr < 2; ++hr) {
-          const uint64_t dot = pack_f32x2(s[rt][j][2 * hr], s[rt][j][2 * hr + 1]);
-          const float2 x = f32x2_parts(f32x2_fma(f32x2_mul(dot, rf2[hr]), f, lv));
-          s[rt][j][2 * hr] = x.x;
-          s[rt][j][2 * hr + 1] = x.y;
-        }
-      }
-      if (!all_seen) {
-#pragma unroll
-        for (int hr = 0; hr < 2; ++hr) {
-          const int row = min(row0 + rt * 16 + (lane >> 2) + hr * 8, p.rows - 1);
-          const int own = intra ? T : T * p.n + p.s0 + q_row(p, grp, hk, row).s;
-#pragma unroll
-          for (int j = 0; j < kQTile / 8; ++j)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int c = base + j * 8 + (lane & 3) * 2 + e;
-              if (!(c < ce && c <= own && own - c < p.win)) s[rt][j][2 * hr + e] = -INFINITY;
-            }
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < kQTile / 8; ++j)
-#pragma unroll
-        for (int hr = 0; hr < 2; ++hr) mx[hr] = fmaxf(mx[hr], fmaxf(s[rt][j][2 * hr], s[rt][j][2 * hr + 1]));
-      if (__any_sync(0xffffffffu, mx[0] > m_run[rt][0] + 15.f || mx[1] > m_run[rt][1] + 15.f)) {
-#pragma unroll
-        for (int hr = 0; hr < 2; ++hr) {
-          float m = fmaxf(mx[hr], __shfl_xor_sync(0xffffffffu, mx[hr], 1));
-          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-          if (m > m_run[rt][hr] + 15.f) {
-            const float alpha = fast_exp2(m_run[rt][hr] - (m - 13.f));
-            m_run[rt][hr] = m - 13.f;
-            const float2 l = f32x2_parts(l_run[rt][hr]);
-            l_run[rt][hr] = pack_f32x2(l.x * alpha, l.y * alpha);
-#pragma unroll
-            for (int c = 0; c < D / 16; ++c)
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                o[rt][c][h][2 * hr] *= alpha;
-                o[rt][c][h][2 * hr + 1] *= alpha;
-              }
-          }
-        }
-      }
-#pragma unroll
-      for (int hr = 0; hr < 2; ++hr) {
-        const float mu = m_run[rt][hr] == -INFINITY ? 0.f : -m_run[rt][hr];
-        const uint64_t mu2 = pack_f32x2(mu, mu);
-#pragma unroll
-        for (int j = 0; j < kQTile / 8; ++j) {
-          const uint64_t iv = lds64(sFac + (2 * kQTile + j * 8 + (lane & 3) * 2) * 4);
-          const float2 x = f32x2_parts(f32x2_add(pack_f32x2(s[rt][j][2 * hr], s[rt][j][2 * hr + 1]), mu2));
-          const float w0 = fast_exp2(x.x), w1 = fast_exp2(x.y);
-          l_run[rt][hr] = f32x2_fma(pack_f32x2(w0, w1), iv, l_run[rt][hr]);
-          a[rt][j / 2][2 * (j & 1) + hr] = pack_half(w0, w1);
-        }
-      }
-    }
-#pragma unroll
-    for (int k16 = 0; k16 < kQTile / 16; ++k16)
-#pragma unroll
-      for (int c = 0; c < D / 16; c += 2) {  // 16 keys, 32 of d
-        uint32_t r[4];
-        ldsm_x4_t(vb + swz8<D>(k16 * 16 + (lane & 15), c + (lane >> 4)), r[0], r[1], r[2], r[3]);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          uint32_t e0, o0, e1, o1;
-          to_half<FMT, false>(r[2 * i], e0, o0);
-          to_half<FMT, false>(r[2 * i + 1], e1, o1);
-#pragma unroll
-          for (int rt = 0; rt < RT; ++rt) {
-            mma_f16_16816(o[rt][c + i][0], a[rt][k16], e0, e1);
-            mma_f16_16816(o[rt][c + i][1], a[rt][k16], o0, o1);
-          }
-        }
-      }
+    const Q8Seen seen = {base + kQTile <= ce && base + kQTile - 1 <= pmin && pmax - base < p.win,
+                         base, ce, p.win, intra ? T : T * p.n + p.s0, intra ? 0 : p.g, row0, p.rows - 1};
+    rows.tile(sQ, kb, vb, sFac, seen, lane);
     __syncwarp();  // every lane has read the tile and its scales before the next ones replace them
     if (lane == 0 && done + S < tiles) load(done + S);
   }
@@ -552,24 +757,7 @@ __global__ void __launch_bounds__(kQThreads, Q8Smem<D, RT>::CTAS)
   // ---- merge the warps' states in shared memory: per warp [ROWS][D+4] floats
   float* mbuf = reinterpret_cast<float*>(smem);
   constexpr int RS = D + 4;
-#pragma unroll
-  for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-    for (int hr = 0; hr < 2; ++hr) {
-      const float2 lp = f32x2_parts(l_run[rt][hr]);
-      float l = lp.x + lp.y;
-      l += __shfl_xor_sync(0xffffffffu, l, 1);
-      l += __shfl_xor_sync(0xffffffffu, l, 2);
-      float* rowp = mbuf + (warp * ROWS + rt * 16 + (lane >> 2) + hr * 8) * RS;
-      if ((lane & 3) == 0) {
-        rowp[D] = m_run[rt][hr];
-        rowp[D + 1] = l;
-      }
-#pragma unroll
-      for (int c = 0; c < D / 16; ++c)
-        *reinterpret_cast<float4*>(rowp + c * 16 + (lane & 3) * 4) =
-            make_float4(o[rt][c][0][2 * hr], o[rt][c][1][2 * hr], o[rt][c][0][2 * hr + 1], o[rt][c][1][2 * hr + 1]);
-    }
+  rows.store(mbuf + warp * ROWS * RS, lane);
   __syncthreads();
   if (*abort_flag) return;
   const bool all = r1 - r0 == rounds;
@@ -747,18 +935,18 @@ bool make_map(CUtensorMap* map, const uint8_t* base, long long J, long long R, l
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, int FMT, int RT>
+template <int D, int FMT, int TR>
 cudaError_t launch_decode_q8_d(const DecodeQ8Params& p, cudaStream_t stream) {
   const bool intra = p.kpt == 1 && p.n > 1;
   const long long J = intra ? static_cast<long long>(p.n) * p.Hkv : p.Hkv;
   const long long R = intra ? p.Tcap : static_cast<long long>(p.Tcap) * p.n;
   CUtensorMap mk, mv;
   if (!make_map<D>(&mk, p.kc, J, R, p.B) || !make_map<D>(&mv, p.vc, J, R, p.B)) return cudaErrorInvalidValue;
-  const int smem = Q8Smem<D, RT>::TOTAL;
-  cudaError_t e = cudaFuncSetAttribute(decode_q8_split_kernel<D, FMT, RT>,
+  const int smem = Q8Smem<D, TR>::TOTAL;
+  cudaError_t e = cudaFuncSetAttribute(decode_q8_split_kernel<D, FMT, TR>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  decode_q8_split_kernel<D, FMT, RT><<<static_cast<unsigned>(p.ctas * p.Hkv * p.mt), kQThreads, smem, stream>>>(p, mk, mv);
+  decode_q8_split_kernel<D, FMT, TR><<<static_cast<unsigned>(p.ctas * p.Hkv * p.mt), kQThreads, smem, stream>>>(p, mk, mv);
   e = cudaGetLastError();
   if (e != cudaSuccess || p.whole) return e;
   cudaLaunchAttribute attr = {};
@@ -775,15 +963,16 @@ cudaError_t launch_decode_q8_d(const DecodeQ8Params& p, cudaStream_t stream) {
 
 template <int D, int FMT>
 cudaError_t launch_decode_q8_rt(const DecodeQ8Params& p, cudaStream_t stream) {
-  if (p.tile_rows == 16) return launch_decode_q8_d<D, FMT, 1>(p, stream);
-  if (p.tile_rows == 32) return launch_decode_q8_d<D, FMT, 2>(p, stream);
+  if (p.tile_rows == 8) return launch_decode_q8_d<D, FMT, 8>(p, stream);
+  if (p.tile_rows == 16) return launch_decode_q8_d<D, FMT, 16>(p, stream);
+  if (p.tile_rows == 32) return launch_decode_q8_d<D, FMT, 32>(p, stream);
   return cudaErrorInvalidValue;
 }
 
 }  // namespace
 
 // Rows of a CTA.
-int decode_q8_tile_rows(int rows) { return rows <= 16 ? 16 : 32; }
+int decode_q8_tile_rows(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
 
 // CTAs of a line (of `lines` KV heads and row tiles), the rounds that a piece has at
 // least, and whether each CTA takes one problem whole instead of a piece: where
