@@ -288,7 +288,7 @@ size_t decode_q8_problem(DecodeQ8Params& p, int mode, int W_tokens, int final_on
   p.tile_rows = decode_q8_tile_rows(p.rows);
   p.mt = (p.rows + p.tile_rows - 1) / p.tile_rows;
   const long long problems = static_cast<long long>(p.B) * p.groups;
-  decode_q8_plan(problems, keys, p.tile_rows, static_cast<long long>(p.Hkv) * p.mt, sm_count(), &p.ctas, &p.least,
+  decode_q8_plan(problems, keys, p.D, p.tile_rows, static_cast<long long>(p.Hkv) * p.mt, sm_count(), &p.ctas, &p.least,
                  &p.whole);
   p.slots = static_cast<int>(problems) + p.ctas;
   const size_t prow = p.whole ? 1 : static_cast<size_t>(p.mt) * p.Hkv * p.tile_rows * p.slots;  // (never empty)

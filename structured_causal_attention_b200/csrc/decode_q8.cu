@@ -26,20 +26,30 @@
 //
 // Under INTRA each stream is a problem of its own (g query rows, every n-th
 // position), so every loaded key is visible and none is read twice; otherwise
-// the n*g rows of a KV head share the keys.
+// the n*g rows of a KV head share the keys. A CTA has a tile of 8, 16 or 32 rows: a
+// tile of 8 is the N of the MMAs (half the MMAs and exponentials of 16 rows that
+// are half padding: 200 -> 190 us, and with two CTAs an SM 176), 16 are their M,
+// and of 32 the codes are converted once for two such M (B8, 8192 tokens, 32 rows:
+// 194 -> 141 us). One mma.sync tile of rows is all that the keys meet, so tcgen05's
+// M of 64 and more would be padding, and its operands 8-bit terms (see above).
 //
 // The work is one line of rounds of 128 keys for each KV head: all rounds of the
 // first problem (sequence, stream group), then of the next, as the lengths on the
 // device have it. As many CTAs as fit the GPU at once each take an equal piece of
-// a head's line, whatever the lengths, so a ragged batch keeps every SM busy. The
-// heads' CTAs walk their lines side by side, as neighbouring heads lie side by
-// side in a row of the cache: with one line through all heads in turn, whose
-// rows are then fetched in scattered pieces of 128 (64) bytes, a step at D = 128
-// took 10% longer and at D = 64 30%. Within a
+// a head's line, whatever the lengths, so a ragged batch keeps every SM busy (the
+// ragged final INTRA step: 49 -> 42 us). The heads' CTAs walk their lines side by
+// side, as neighbouring heads lie side by side in a row of the cache: with one
+// line through all heads in turn, whose rows are then fetched in scattered pieces
+// of 128 (64) bytes, a step at D = 128 took 10% longer and at D = 64 30%. Within a
 // problem a CTA's warps each stream 32-key tiles of their own through a TMA ring
 // of their own, with nothing between warps until their states are merged. A
-// problem that one CTA has whole is written by it; of the others each piece goes
+// problem that one CTA has whole is written by it; of the others each part goes
 // to the workspace, and a second kernel joins them.
+//
+// HBM bounds it, at the power cap's clock with the conversions close behind:
+// B8, 16385 tokens, 32/8 heads of 128, 1.08 GB: 192 us E4M3 (5.6 TB/s), its
+// final-stream step 176 us (6.1 TB/s); B64 INT8, 8.6 GB, 1.58 ms (5.4 TB/s; 1.37 ms,
+// 6.3 TB/s, before the clock falls).
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -57,16 +67,19 @@ constexpr int kQTile = 32;  // keys of a warp's tile
 static_assert(kQWarps * kQTile == kQ8Round, "a round");
 constexpr float kLn2 = 0.69314718055994530942f;
 
-// CTAs of an SM. Three hide more latency than two: 64 sequences of 16385 tokens in
-// INT8 took 1574 us with three and 1650 with two, 8 in E4M3 191 and 196, at D = 64
-// 105 and 118. Two row tiles need the registers of two.
-constexpr int q8_ctas_per_sm(int tile_rows) { return tile_rows <= 16 ? 3 : 2; }
+// CTAs of an SM. The copies that three keep in flight are more than HBM serves
+// best, but a tile of 16 rows has so much to compute that three are faster all the
+// same: 64 sequences of 16385 tokens in INT8 took 1574 us with three and 1650 with
+// two, 8 in E4M3 191 and 196. With 8 rows two are: 8 sequences' final streams 190
+// and 176. At D = 64, with tiles of half the bytes, three are (102 and 111 us).
+// Two row tiles need the registers of two.
+constexpr int q8_ctas_per_sm(int D, int tile_rows) { return tile_rows == 32 || (tile_rows == 8 && D == 128) ? 2 : 3; }
 
 // TR query rows a CTA: 8, 16 or 32 (two tiles of 16, the codes converted once for
 // both).
 template <int D, int TR>
 struct Q8Smem {
-  static constexpr int CTAS = q8_ctas_per_sm(TR);
+  static constexpr int CTAS = q8_ctas_per_sm(D, TR);
   static constexpr int KV = kQTile * D;              // bytes of K (or V) of a tile
   static constexpr int STAGES = (TR <= 16 ? 2 : 3) * (128 / D);
   static constexpr int RING = kQWarps * STAGES * 2 * KV;
@@ -920,6 +933,7 @@ EncodeTiledFn encode_fn() {
 }
 
 // The codes as (d, head or (stream, head), row, sequence), a box of one tile.
+// Promotion to 256 bytes brings the next head's row of a key along: 206 -> 195 us.
 template <int D>
 bool make_map(CUtensorMap* map, const uint8_t* base, long long J, long long R, long long B) {
   EncodeTiledFn fn = encode_fn();
@@ -977,11 +991,12 @@ int decode_q8_tile_rows(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
 // CTAs of a line (of `lines` KV heads and row tiles), the rounds that a piece has at
 // least, and whether each CTA takes one problem whole instead of a piece: where
 // none has more than kWhole rounds, dividing one and joining its parts takes
-// longer than it saves, and the second kernel is left out.
-void decode_q8_plan(long long problems, long long most_keys, int tile_rows, long long lines, int sms, int* ctas,
+// longer than it saves (B8, 8 rounds: 14.3 us and 13.0; 16 rounds: 15.4 and 21), and
+// the second kernel is left out.
+void decode_q8_plan(long long problems, long long most_keys, int D, int tile_rows, long long lines, int sms, int* ctas,
                     int* least, int* whole) {
   constexpr int kWhole = 8;
-  const long long slots = sms * q8_ctas_per_sm(tile_rows) / lines;
+  const long long slots = sms * q8_ctas_per_sm(D, tile_rows) / lines;
   *whole = most_keys <= kWhole * kQ8Round;
   *least = 2;
   *ctas = static_cast<int>(*whole ? problems : (slots > 1 ? slots : 1));

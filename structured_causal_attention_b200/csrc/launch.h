@@ -123,7 +123,7 @@ struct DecodeQ8Params {
 };
 constexpr int kQ8Round = 128;  // keys that a CTA's warps take at once
 int decode_q8_tile_rows(int rows);
-void decode_q8_plan(long long problems, long long most_keys, int tile_rows, long long lines, int sms, int* ctas,
+void decode_q8_plan(long long problems, long long most_keys, int D, int tile_rows, long long lines, int sms, int* ctas,
                     int* least, int* whole);
 cudaError_t launch_decode_q8(const DecodeQ8Params& p, cudaStream_t stream);
 
