@@ -273,12 +273,13 @@ def _cache_q8(cache):
     _need_cuda(k, v, k_scale, v_scale)
     if v.dtype != k.dtype or k.dtype not in (torch.float8_e4m3fn, torch.int8):
         raise ValueError("codes must be float8_e4m3fn or int8, k and v alike")
-    if n < 1 or block_tokens < 1 or k.dim() != 4 or k.shape[1] % n:
+    shape = k.shape
+    if n < 1 or block_tokens < 1 or len(shape) != 4 or shape[1] % n:
         raise ValueError("codes must be [B, Tcap*n, Hkv, D]")
-    B, S, Hkv, D = k.shape
+    B, S, Hkv, D = shape
     Tcap = S // n
     want = (B, Hkv, -(-Tcap // block_tokens), n)
-    if v.shape != k.shape or k_scale.shape != want or v_scale.shape != want:
+    if v.shape != shape or k_scale.shape != want or v_scale.shape != want:
         raise ValueError(f"k and v must be alike and the scales {list(want)}")
     if k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32:
         raise ValueError("scales must be float32")
@@ -317,11 +318,12 @@ def kv_write_q8(k, v, cache, token_offset=None, lengths=None, stream=None):
     B, Tcap, Hkv, D, fmt = _cache_q8(cache)
     if k.dtype != torch.bfloat16 or v.dtype != torch.bfloat16:
         raise ValueError("k and v must be bfloat16")
-    if k.dim() != 4 or k.shape != v.shape or k.shape[0] != B or k.shape[2:] != (Hkv, D) or k.shape[1] % cache.n:
+    shape = k.shape
+    L = shape[1] // cache.n if len(shape) == 4 else 0
+    if shape != (B, L * cache.n, Hkv, D) or v.shape != shape:
         raise ValueError(f"k and v must be [{B}, L*{cache.n}, {Hkv}, {D}]")
     _index_q8(token_offset, B, "token_offset")
     _index_q8(lengths, B, "lengths")
-    L = k.shape[1] // cache.n
     codes = cache[:4]
     if L:
         _call_on((*codes, k, v, token_offset, lengths), hd_kv_write_q8, k, v, token_offset, lengths, *codes, B, L,
@@ -357,12 +359,13 @@ def _decode_q8(q, cache, seqlen, mode, W, scale, stream, workspace, final):
     B, Tcap, Hkv, D, fmt = _cache_q8(cache)
     n = cache.n
     nq = 1 if final else n
-    if q.dtype != torch.bfloat16 or q.dim() != 4 or q.shape[:2] != (B, nq) or q.shape[3] != D:
+    shape = q.shape
+    Hq = shape[2] if len(shape) == 4 else 0
+    if q.dtype != torch.bfloat16 or shape != (B, nq, Hq, D):
         raise ValueError(f"q must be bfloat16 [{B}, {nq}, Hq, {D}]")
     _index_q8(seqlen, B, "seqlen")
     if workspace is not None:
         _need_cuda(workspace)
-    Hq = q.shape[2]
     if scale is None:
         scale = D ** -0.5
     out = torch.empty_like(q)
