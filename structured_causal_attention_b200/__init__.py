@@ -300,6 +300,18 @@ def _call_on(ts, call, *args):
         return call(*args)
 
 
+def _within(stream, device):
+    """``stream`` (a torch stream or a handle) as the current one: a context. What is allocated in it is the
+    stream's own, so that no other stream is given the memory while the stream's kernels use it."""
+    import torch
+
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device) if stream else torch.cuda.default_stream(device)
+    if stream.device != device:
+        raise ValueError("the stream must be of the tensors' device")
+    return torch.cuda.stream(stream)
+
+
 def _index_q8(t, B, what):
     import torch
 
@@ -316,6 +328,9 @@ def kv_write_q8(k, v, cache, token_offset=None, lengths=None, stream=None):
 
     _need_cuda(k, v)
     B, Tcap, Hkv, D, fmt = _cache_q8(cache)
+    if stream is not None:
+        with _within(stream, k.device):
+            return kv_write_q8(k, v, cache, token_offset, lengths)
     if k.dtype != torch.bfloat16 or v.dtype != torch.bfloat16:
         raise ValueError("k and v must be bfloat16")
     shape = k.shape
@@ -327,7 +342,7 @@ def kv_write_q8(k, v, cache, token_offset=None, lengths=None, stream=None):
     codes = cache[:4]
     if L:
         _call_on((*codes, k, v, token_offset, lengths), hd_kv_write_q8, k, v, token_offset, lengths, *codes, B, L,
-                 cache.n, Tcap, Hkv, D, fmt, cache.block_tokens, stream)
+                 cache.n, Tcap, Hkv, D, fmt, cache.block_tokens)
 
 
 def kv_read_q8(cache, L, token_offset=None, lengths=None, out=None, stream=None):
@@ -336,6 +351,9 @@ def kv_read_q8(cache, L, token_offset=None, lengths=None, out=None, stream=None)
     import torch
 
     B, Tcap, Hkv, D, fmt = _cache_q8(cache)
+    if stream is not None:
+        with _within(stream, cache.k.device):
+            return kv_read_q8(cache, L, token_offset, lengths, out)
     _index_q8(token_offset, B, "token_offset")
     _index_q8(lengths, B, "lengths")
     shape = (B, L * cache.n, Hkv, D)
@@ -348,7 +366,7 @@ def kv_read_q8(cache, L, token_offset=None, lengths=None, out=None, stream=None)
     codes = cache[:4]
     if L:
         _call_on((*codes, token_offset, lengths, k, v), hd_kv_read_q8, *codes, token_offset, lengths, k, v, B, L,
-                 cache.n, Tcap, Hkv, D, fmt, cache.block_tokens, stream)
+                 cache.n, Tcap, Hkv, D, fmt, cache.block_tokens)
     return k, v
 
 
@@ -356,6 +374,9 @@ def _decode_q8(q, cache, seqlen, mode, W, scale, stream, workspace, final):
     import torch
 
     _need_cuda(q, seqlen)
+    if stream is not None:
+        with _within(stream, q.device):
+            return _decode_q8(q, cache, seqlen, mode, W, scale, None, workspace, final)
     B, Tcap, Hkv, D, fmt = _cache_q8(cache)
     n = cache.n
     nq = 1 if final else n
@@ -375,7 +396,7 @@ def _decode_q8(q, cache, seqlen, mode, W, scale, stream, workspace, final):
     codes = cache[:4]
     _call_on((q, *codes, seqlen, workspace), hd_decode_attn_final_q8 if final else hd_decode_attn_q8, q, *codes, seqlen,
              out, lse, B, n, Tcap, Hq, Hkv, D, fmt, cache.block_tokens, mode, W, scale, workspace,
-             workspace.numel() * workspace.element_size(), stream)
+             workspace.numel() * workspace.element_size())
     return out, lse
 
 

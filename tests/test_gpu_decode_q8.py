@@ -328,3 +328,31 @@ def test_cache_past_32_bits(fmt):
     out, lse = _attend(q[:, -1:], cache, seqlen, hd.CROSS_WINDOW, 16, 0.1, True)
     tail = hd.KVCacheQ8(cache.k[1:, -16 * n:], cache.v[1:, -16 * n:], cache.k_scale[1:, :, -1:], cache.v_scale[1:, :, -1:], n, bt)
     check_attention(out[1:], lse[1:], q[1:, -1:], on_host(tail), n, bt, fmt, torch.tensor([16]), hd.CROSS_FULL, 0, 0.1, True)
+
+
+@pytest.mark.parametrize("as_handle", [False, True], ids=["stream", "handle"])
+def test_memory_of_a_call_on_another_stream_is_its_own(as_handle):
+    """A call on a stream that is still busy: what the caller allocates and writes meanwhile does not reach it."""
+    need_gpu()
+    B, n, T, Hq, Hkv, D = 2, 4, 1500, 16, 4, 64
+    seqlen = _lengths(B, T, 3, False).cuda()
+    cache = _filled(B, T, n, Hkv, D, "int8", 16, seqlen.cpu(), 4)
+    q = syn.normal_bf16((B, n, Hq, D), 5).cuda()
+    alone = hd.decode_attn_q8(q, cache, seqlen, hd.CROSS_FULL)
+    read = hd.kv_read_q8(cache, 100)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    s = side.cuda_stream if as_handle else side
+    size = hd.hd_decode_q8_workspace_bytes(B, n, T, Hq, Hkv, D)
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)  # ~10 ms
+    out, lse = hd.decode_attn_q8(q, cache, seqlen, hd.CROSS_FULL, stream=s)
+    k, v = hd.kv_read_q8(cache, 100, stream=s)
+    others = [torch.full((size,), 0xFF, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    side.synchronize()
+    assert torch.equal(out, alone[0]) and torch.equal(lse, alone[1])
+    assert torch.equal(k, read[0]) and torch.equal(v, read[1])
+    assert all(bool((x == 0xFF).all()) for x in others)
+    zero = hd.decode_attn_q8(q, cache, seqlen, hd.CROSS_FULL, stream=0)
+    torch.cuda.synchronize()
+    assert torch.equal(zero[0], alone[0])
