@@ -382,7 +382,8 @@ int hd_kv_read_q8(const void* k_codes, const void* v_codes, const float* k_scale
                   int n, int Tcap, int Hkv, int D, int format, int block_tokens, void* stream);
 
 /* Bytes of workspace hd_decode_attn_q8 and hd_decode_attn_final_q8 need for
- * these sizes, whatever the mode, format and block_tokens (0 on invalid sizes). */
+ * these sizes, whatever the mode, format and block_tokens (0 on sizes that they
+ * refuse). */
 size_t hd_decode_q8_workspace_bytes(int B, int n, int Tcap, int Hq, int Hkv, int D);
 size_t hd_decode_final_q8_workspace_bytes(int B, int n, int Tcap, int Hq, int Hkv, int D);
 
@@ -392,7 +393,8 @@ size_t hd_decode_final_q8_workspace_bytes(int B, int n, int Tcap, int Hq, int Hk
  * q, seqlen, out, lse, mode, W_tokens, scale, the precondition (the new token's
  * n rows are in the cache) and the errors are theirs; the cache is as above.
  * Scores and softmax are fp32 and the scales are applied in fp32; the weights
- * are rounded to fp16 before they meet the V codes. Supported: as there.
+ * are rounded to fp16 before they meet the V codes. Supported: as there, with
+ * B*n*Hq*ceil(Tcap*n / 128) <= 2^30 and Tcap*n*Hkv*D < 2^40.
  */
 int hd_decode_attn_q8(const void* q, const void* k_codes, const void* v_codes, const float* k_scale,
                       const float* v_scale, const int32_t* seqlen, void* out, float* lse, int B, int n,

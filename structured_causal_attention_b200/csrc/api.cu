@@ -296,10 +296,25 @@ size_t decode_q8_problem(DecodeQ8Params& p, int mode, int W_tokens, int final_on
   return align256(prow * static_cast<size_t>(p.D) * 4) + align256(prow * 2 * 4);
 }
 
+// The sizes that a decode step over the 8-bit cache takes. Each product is formed
+// after those that bound its factors.
+int check_decode_q8(int B, int n, int Tcap, int Hq, int Hkv, int D) {
+  if (B < 1 || n < 1 || Tcap < 1 || Hq < 1 || Hkv < 1 || D < 1 || Hq % Hkv != 0) return HD_ERR_INVALID_ARG;
+  const long long positions = static_cast<long long>(Tcap) * n;
+  if (positions > kMaxPositions || (D != 64 && D != 128)) return HD_ERR_UNSUPPORTED;
+  // rows of the output and rounds of the line are counted in 32 bits
+  constexpr long long kMost = 1LL << 30;
+  const long long heads = static_cast<long long>(n) * Hq;
+  if (heads > kMost || heads * B > kMost) return HD_ERR_UNSUPPORTED;
+  if (heads * B * ((positions + kQ8Round - 1) / kQ8Round) > kMost) return HD_ERR_UNSUPPORTED;
+  if (positions * Hkv * D >= 1LL << 40) return HD_ERR_UNSUPPORTED;  // a TMA stride
+  return HD_OK;
+}
+
 // The most that any mode and window needs. (A window's pieces are no more than
 // those of the whole cache.)
 size_t decode_q8_workspace(int B, int n, int Tcap, int Hq, int Hkv, int D, int final_only) {
-  if (B < 1 || n < 1 || Tcap < 1 || Hq < 1 || Hkv < 1 || D < 1 || Hq % Hkv) return 0;
+  if (check_decode_q8(B, n, Tcap, Hq, Hkv, D) != HD_OK) return 0;
   size_t most = 0;
   for (int mode = HD_INTRA; mode <= HD_CROSS_FULL; ++mode) {
     DecodeQ8Params p = {};
@@ -324,18 +339,14 @@ int decode_q8_call(const void* q, const void* k_codes, const void* v_codes, cons
     return HD_ERR_INVALID_ARG;
   const int st = check_q8(B, n, Tcap, Hkv, D, format, block_tokens);
   if (st != HD_OK) return st;
-  if (Hq < 1 || Hq % Hkv != 0) return HD_ERR_INVALID_ARG;
   if (mode < HD_INTRA || mode > HD_CROSS_WINDOW) return HD_ERR_INVALID_ARG;
   if (mode == HD_CROSS_WINDOW && W_tokens < 1) return HD_ERR_INVALID_ARG;
   if (!(scale > 0.f) || !isfinite(scale)) return HD_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(k_codes) || !aligned16(v_codes) || !aligned16(k_scale) ||
       !aligned16(v_scale) || !aligned16(out) || !aligned16(workspace))
     return HD_ERR_INVALID_ARG;
-  if (static_cast<long long>(Tcap) * n * Hkv * D >= 1LL << 40) return HD_ERR_UNSUPPORTED;  // a TMA stride
-  // rows of the output and rounds of the line are counted in 32 bits
-  const long long per_token = static_cast<long long>(B) * n * Hq;
-  if (per_token > 1LL << 30 || per_token * ((static_cast<long long>(Tcap) * n + kQ8Round - 1) / kQ8Round) > 1LL << 30)
-    return HD_ERR_UNSUPPORTED;
+  const int fits = check_decode_q8(B, n, Tcap, Hq, Hkv, D);
+  if (fits != HD_OK) return fits;
   if (workspace_bytes < decode_q8_workspace(B, n, Tcap, Hq, Hkv, D, final_only)) return HD_ERR_INVALID_ARG;
   DecodeQ8Params p = {};
   p.q = static_cast<const __nv_bfloat16*>(q);

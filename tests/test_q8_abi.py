@@ -81,3 +81,20 @@ def test_binding_raises_on_error(lib):
     with pytest.raises(hd.HDError) as e:
         hd.hd_kv_write_q8(FAKE, FAKE, 0, 0, FAKE, FAKE, FAKE, FAKE, 1, 8, 4, 64, 2, 96, 0, 16, stream=0)
     assert e.value.status == hd.HD_ERR_UNSUPPORTED
+
+
+# (each of these has a product that passes 32 or 64 bits; the queries' rows of the first come to 2^32)
+@pytest.mark.parametrize("sizes", [
+    (1, 65536, 1, 65536, 1, 64), (2**31 - 1, 2**28, 1, 2**31 - 1, 1, 128), (2**31 - 1, 1, 1, 2, 1, 64),
+    (1, 1, 2**28, 2**31 - 1, 2**31 - 1, 128), (1, 1, 2**31 - 1, 1, 1, 64), (1, 2, 1, 2**30, 1, 64),
+    (8, 4, 2**26, 32, 8, 128), (1, 1, 100, 4, 4, 2**31 - 1),
+])
+@pytest.mark.parametrize("final", [False, True], ids=["streams", "final"])
+def test_sizes_past_the_counters_are_refused(lib, final, sizes):
+    """No product of sizes wraps: the workspace's size is 0 and the call refused, for each mode."""
+    size = hd.hd_decode_final_q8_workspace_bytes if final else hd.hd_decode_q8_workspace_bytes
+    assert size(*sizes) == 0
+    fn = lib.hd_decode_attn_final_q8 if final else lib.hd_decode_attn_q8
+    for mode in (hd.INTRA, hd.CROSS_FULL, hd.CROSS_WINDOW):
+        st = fn(*[FAKE] * 8, *sizes, hd.HD_Q8_INT8, 16, mode, 1, 0.1, FAKE, 2**63, None)
+        assert st == hd.HD_ERR_UNSUPPORTED
