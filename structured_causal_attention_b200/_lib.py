@@ -111,7 +111,11 @@ def ptr(x) -> int:
     try:
         return x.data_ptr()
     except AttributeError:
-        return 0 if x is None else x
+        if x is None:
+            return 0
+        if isinstance(x, int):
+            return x
+        raise  # (a str or bytes would pass as a host address)
 
 
 def stream_handle(stream) -> int:

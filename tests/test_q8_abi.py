@@ -98,3 +98,11 @@ def test_sizes_past_the_counters_are_refused(lib, final, sizes):
     for mode in (hd.INTRA, hd.CROSS_FULL, hd.CROSS_WINDOW):
         st = fn(*[FAKE] * 8, *sizes, hd.HD_Q8_INT8, 16, mode, 1, 0.1, FAKE, 2**63, None)
         assert st == hd.HD_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("other", ["0x10000", b"0x10000", 65536.0, [FAKE]])
+def test_only_tensors_and_addresses_are_pointers(lib, other):
+    """Text and bytes are no device pointers, though ctypes would pass their host address."""
+    assert hd._lib.ptr(None) == 0 and hd._lib.ptr(FAKE) == FAKE
+    with pytest.raises(AttributeError):
+        hd._lib.ptr(other)
