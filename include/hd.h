@@ -357,7 +357,9 @@ typedef enum { HD_Q8_E4M3 = 0, HD_Q8_INT8 = 1 } hd_q8_format;
  * A block whose first token is written starts afresh, whatever it held. A block
  * that was begun before keeps its scale or, where the new rows need a larger
  * one, is raised to that, and the codes of its earlier tokens are rounded
- * again, code * old / new. Codes of other tokens stay as they are.
+ * again, code * old / new. Codes of other tokens stay as they are. (A block
+ * that is entered behind its first token, with that never written, has to hold
+ * a scale of 0.)
  * If a written row holds a NaN or an infinity, its block's scale of that stream
  * and head becomes NaN (and stays so until the block starts afresh): every
  * value of it reads as NaN, and so does each attention output that sees one.
@@ -371,7 +373,9 @@ int hd_kv_write_q8(const void* k, const void* v, const int32_t* token_offset, co
                    int Tcap, int Hkv, int D, int format, int block_tokens, void* stream);
 
 /*
- * hd_kv_read_q8 - rows of the 8-bit cache as bf16 (code * scale, rounded).
+ * hd_kv_read_q8 - rows of the 8-bit cache as bf16 (code * scale, rounded; what
+ * is behind the largest bf16 value, which a code of a value within 3% of it can
+ * be, reads as infinity).
  * Arguments as hd_kv_write_q8, with k, v the outputs, bf16 [B, L*n, Hkv, D]:
  * tokens token_offset[b] .. token_offset[b] + lengths[b] - 1. Rows behind
  * lengths[b], and all of a sequence whose range lies outside the cache

@@ -112,6 +112,28 @@ def test_every_scale_border_and_tie(fmt):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
+def test_the_largest_values(fmt):
+    """Rows up to bf16's largest value, 255 * 2^120: codes and scales are the definition's, and a code whose value
+    rounds past it (256 * 2^120 in E4M3, 127 scales in INT8) reads as infinity. A code times its scale has at
+    most 15 significant bits, so fp32 holds it and the one rounding is the one to bf16."""
+    need_gpu()
+    D, n = 64, 1
+    tops = [m * 2.0 ** 120 for m in range(128, 256)]
+    share = torch.arange(D, 0, -1, dtype=torch.float64) / D
+    k = torch.stack([share * a for a in tops]).reshape(1, len(tops), 1, D)
+    k[..., 1::2] *= -1
+    k = k.to(torch.float32).to(torch.bfloat16)
+    assert k.isfinite().all() and k[0, -1, 0, 0] == torch.finfo(torch.bfloat16).max
+    cache = garbage_cache(1, len(tops), n, 1, D, fmt, 1)
+    host = _write(cache, on_host(cache), k, -k, fmt)
+    same_cache(cache, host)
+    for got, name in zip(hd.kv_read_q8(cache, len(tops)), "kv"):
+        want = torch.tensor(oracle.kv_read_q8(*host[name], n, 1, fmt, len(tops))).to(torch.float32).to(torch.bfloat16)
+        assert want.isinf().any() and torch.equal(got.cpu(), want)
+    assert hd.hd_device_status() == hd.HD_OK
+
+
+@pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
 def test_a_value_that_is_no_number_marks_its_block(fmt, bad):
     """The block's scale of that stream and head is NaN, stays so for later rows, and goes when it starts afresh."""
