@@ -279,11 +279,11 @@ struct Q8Rows {
   float m_run[RT][2];
   uint64_t l_run[RT][2];  // two partial sums a row
 
-  __device__ __forceinline__ void start(uint32_t, const float* row_fac, int lane) {
+  __device__ __forceinline__ void start(uint32_t, const float* row_fac, float down, int lane) {
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
 #pragma unroll
-      for (int hr = 0; hr < 2; ++hr) rf[rt][hr] = row_fac[rt * 16 + (lane >> 2) + hr * 8];
+      for (int hr = 0; hr < 2; ++hr) rf[rt][hr] = row_fac[rt * 16 + (lane >> 2) + hr * 8] * down;
 #pragma unroll
       for (int c = 0; c < D / 16; ++c)
 #pragma unroll
@@ -449,8 +449,8 @@ struct Q8Rows8 {
   float m_run[2];
   uint64_t l_run;         // of rows 2t, 2t+1, over this lane's keys
 
-  __device__ __forceinline__ void start(uint32_t sQ, const float* row_fac, int lane) {
-    rf = pack_f32x2(row_fac[(lane & 3) * 2], row_fac[(lane & 3) * 2 + 1]);
+  __device__ __forceinline__ void start(uint32_t sQ, const float* row_fac, float down, int lane) {
+    rf = pack_f32x2(row_fac[(lane & 3) * 2] * down, row_fac[(lane & 3) * 2 + 1] * down);
 #pragma unroll
     for (int c = 0; c < D / 16; c += 2)
       ldsm_x4(sQ + swz(lane & 7, c * 2 + (lane >> 3), D / 8), qb[c][0], qb[c][1], qb[c + 1][0], qb[c + 1][1]);
@@ -724,7 +724,15 @@ __global__ void __launch_bounds__(kQThreads, Q8Smem<D, TR>::CTAS)
   }
   __syncthreads();
   typename Q8RowsOf<D, FMT, TR>::type rows;
-  rows.start(sQ, row_fac, lane);
+  // A score is dot * (row's factor) * (key's), from the left, and |dot| < 2^31 (2^15 * 448 * 128). So that no finite
+  // row's product with a code passes fp32 where the score does not, a factor of 2^95 and more (a row of 2^109) is
+  // taken down to 2^95, all rows' by as much, and the keys' factors up. Those then stop at the largest fp32:
+  // scale * scales of 2^110 and more, where that row's scores pass fp32 too or are 0, as they stay.
+  const uint32_t rf_bits = lane < ROWS ? __float_as_uint(row_fac[lane]) : 0u;  // (not negative)
+  const int rf_top = static_cast<int>(__reduce_max_sync(0xffffffffu, rf_bits < 0x7f800000u ? rf_bits : 0u) >> 23) - 127;
+  const int down = max(rf_top - 95, 0);  // at most 18
+  rows.start(sQ, row_fac, __int_as_float((127 - down) << 23), lane);
+  const float key_fac = p.scale_log2 * __int_as_float((127 + down) << 23);
   const uint32_t sFac = sQ + SM::Q + warp * (kQTile * 12);
   float* fac = reinterpret_cast<float*>(smem + SM::RING + SM::Q) + warp * (kQTile * 3);
   int done = 0;  // tiles whose copies have arrived
@@ -738,7 +746,8 @@ __global__ void __launch_bounds__(kQThreads, Q8Smem<D, TR>::CTAS)
       const bool fin = e < 128 && e > -127;
       // A scale that is no number (its block took in one) makes the scores of its
       // visible keys NaN. One of zero (never written) counts as the smallest.
-      fac[lane] = ks * p.scale_log2;
+      const float kf = ks * key_fac;
+      fac[lane] = kf == INFINITY ? __int_as_float(0x7f7fffff) : kf;
       fac[kQTile + lane] = fin ? static_cast<float>(e) + __log2f(__uint_as_float((vbits & 0x007fffffu) | 0x3f800000u))
                                : (e == 128 ? __int_as_float(0x7fffffff) : static_cast<float>(kQ8MinExp));
       fac[2 * kQTile + lane] = fin ? __fdividef(1.f, vs) : (e == 128 ? 1.f : __int_as_float((127 - kQ8MinExp) << 23));
