@@ -22,7 +22,9 @@
 // and again once one passes 2^15, so that weights fit fp16 (rounding 2^-12, kept
 // down to 2^-27 of the largest). The softmax's sum takes the same weights without
 // the scale, l += w_j / vs_j, in fp32. So blocks of very different size need no
-// common scale, and O / l needs no correction.
+// common scale, and O / l needs no correction. A weight below fp32's range counts
+// as none, though in l it may: a CTA that meets scales 2^76 and more apart goes over
+// its piece again in plain fp32 (Q8Again; 13 to 15 ms where the loop takes 0.19).
 //
 // Under INTRA each stream is a problem of its own (g query rows, every n-th
 // position), so every loaded key is visible and none is read twice; otherwise
@@ -268,6 +270,14 @@ struct Q8Seen {
   int t0, g, row0, last;  // own key of row r: t0 + min(row0 + r, last) / g (g = 0: t0)
   __device__ __forceinline__ int own(int r) const { return g ? t0 + min(row0 + r, last) / g : t0; }
 };
+
+// l + x * 2^d for d <= 0 and w = 2^d, also where that is below fp32's range and the
+// product is not: sums of keys whose V scales differ by all that fp32 spans.
+__device__ __forceinline__ float add_scaled(float l, float x, float d, float w) {
+  if (d > -100.f) return fmaf(w, x, l);
+  const float r = fast_exp2(0.5f * d);
+  return fmaf(x * r, r, l);
+}
 
 // The state of a warp with 16 RT query rows: rows are the M of its MMAs.
 template <int D, int FMT, int RT>
@@ -583,9 +593,177 @@ struct Q8RowsOf<D, FMT, 8> {
   using type = Q8Rows8<D, FMT>;
 };
 
+// A CTA's piece: rounds pos .. end-1 of the line, problem after problem; of sequence b,
+// group grp of it, the rounds from r0 on, of `rounds`. (The kernel's own loop is the
+// same over plain variables: these members took 16-row tiles' last registers.)
+struct Q8Walk {
+  int pos, end, b, grp, r0, rounds;
+  // False where there is nothing (for p.whole: where the sequence's length is out of range).
+  __device__ __forceinline__ bool start(const DecodeQ8Params& p, int cta, int lane) {
+    if (p.whole) {  // (a problem a CTA)
+      b = static_cast<int>(p.div_groups.div(cta));
+      grp = cta - b * p.groups;
+      pos = r0 = 0;
+      end = rounds = q8_rounds(p, b);
+      return rounds != 0;
+    }
+    const Q8Line line = q8_line(p, lane);
+    pos = cta * line.piece;
+    end = min(pos + line.piece, line.total);
+    if (pos >= end) return false;
+    b = line.sequence(p, lane, pos, r0);  // r0: rounds of the sequence before pos
+    rounds = q8_rounds(p, b);
+    grp = r0 / rounds;
+    r0 -= grp * rounds;
+    return true;
+  }
+  // The end of this problem's rounds in the piece.
+  __device__ __forceinline__ int last() const { return min(rounds, r0 + end - pos); }
+  __device__ __forceinline__ bool next(const DecodeQ8Params& p) {
+    pos += last() - r0;
+    if (pos >= end) return false;
+    r0 = 0;
+    if (++grp == p.groups) {
+      grp = 0;
+      do ++b;
+      while ((rounds = q8_rounds(p, b)) == 0);  // (one that is left has rounds: pos < end)
+    }
+    return true;
+  }
+};
+
+// A piece in plain fp32, a warp a row: a lane has D / 32 of its elements, the keys
+// follow one another. With the weights w = 2^(s + log2 vs - m), as above, but the sum
+// l formed from the scores themselves: for scales so far apart that w / vs has lost
+// keys that count in l. It stands behind the loop over the piece, as inside it took
+// registers of the tiles' (139 -> 146 us at 32 rows of 8192 tokens).
+template <int D, int FMT, int ROWS>
+struct Q8Again {
+  static constexpr int E = D / 32;
+  // Codes lane*E .. lane*E + E-1 of a row.
+  static __device__ __forceinline__ void codes(const uint8_t* row, int lane, float (&x)[4]) {
+    const uint32_t r = E == 4 ? __ldg(reinterpret_cast<const uint32_t*>(row) + lane)
+                              : __ldg(reinterpret_cast<const uint16_t*>(row) + lane);
+    uint32_t h[2];
+    to_half<FMT, true>(r, h[0], h[1]);
+    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&h[0]));
+    const float2 c = __half22float2(*reinterpret_cast<const __half2*>(&h[1]));
+    x[0] = a.x, x[1] = a.y, x[2] = c.x, x[3] = c.y;
+  }
+
+  static __device__ __noinline__ void run(const DecodeQ8Params& p) {
+    uint32_t block, tid;  // (read again, so that nothing is kept for here)
+    asm volatile("mov.u32 %0, %%ctaid.x;\n mov.u32 %1, %%tid.x;\n" : "=r"(block), "=r"(tid));
+    const uint32_t line_head = p.div_mt.div(block);
+    const int row0 = static_cast<int>(block - line_head * p.mt) * ROWS, valid_rows = min(ROWS, p.rows - row0);
+    const int cta = static_cast<int>(p.div_hkv.div(line_head)), hk = static_cast<int>(line_head) - cta * p.Hkv;
+    const int warp = static_cast<int>(tid >> 5), lane = static_cast<int>(tid & 31);
+    Q8Walk at;
+    at.start(p, cta, lane);
+    do {
+      for (int lr = warp; lr < valid_rows; lr += kQWarps) row(p, at, cta, hk, row0, lr, lane);
+    } while (at.next(p));
+  }
+
+  static __device__ __forceinline__ void row(const DecodeQ8Params& p, const Q8Walk& at, int cta, int hk, int row0, int lr,
+                                             int lane) {
+    const int b = at.b, grp = at.grp;
+    const bool intra = p.kpt == 1 && p.n > 1;
+    const int T = __ldg(p.seqlen + b) - 1, t0 = intra ? T : T * p.n + p.s0;
+    const int own = t0 + (intra ? 0 : static_cast<int>(p.div_g.div(row0 + lr)));
+    const int kbeg = max(0, t0 - p.win + 1);
+    const int from = max(kbeg + at.r0 * kQ8Round, own - p.win + 1);
+    const int to = min(min((T + 1) * p.kpt, kbeg + at.last() * kQ8Round), own + 1);
+    const long long qrow = out_row(p, b, grp, hk, row0 + lr), li = lse_at(p, b, grp, hk, row0 + lr);
+    if (!in_bounds(qrow * D, D, p.ext_q, p.status) || !in_bounds(li, 1, p.ext_lse, p.status)) return;
+    float q[E], o[E];
+    uint32_t am = 0;
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      q[i] = __bfloat162float(p.q[qrow * D + lane * E + i]);
+      o[i] = 0.f;
+      am = max(am, __float_as_uint(fabsf(q[i])));
+    }
+    am = __reduce_max_sync(0xffffffffu, am);
+    const int up = min(14 - (max(static_cast<int>(am >> 23), 1) - 127), 126);  // the row as the loop has it
+    const float rf = am >= 0x7f800000u ? __int_as_float(0x7fffffff) : __int_as_float((127 - up) << 23);
+#pragma unroll
+    for (int i = 0; i < E; ++i) q[i] *= __int_as_float((127 + up) << 23);
+    float m = -INFINITY, l = 0.f;  // l times 2^20: see below
+    // key c's codes are at c steps, and a lane looks up the scales of one key of 32
+    const long long step = static_cast<long long>(intra ? p.n * p.Hkv : p.Hkv) * D;
+    const long long base = (static_cast<long long>(b) * p.Tcap * p.n * p.Hkv +
+                            (intra ? (p.s0 + grp) * p.Hkv + hk : hk)) * static_cast<long long>(D);
+    const uint8_t *kc = p.kc + base, *vc = p.vc + base;
+    const long long sc0 = (static_cast<long long>(b) * p.Hkv + hk) * p.nb * p.n;
+    constexpr int U = 4;  // keys in flight
+    for (int c32 = from; c32 < to; c32 += 32) {
+      const int c = min(c32 + lane, to - 1);
+      const int tok = intra ? c : static_cast<int>(p.div_n.div(c)), st = intra ? p.s0 + grp : c - tok * p.n;
+      const long long si = sc0 + static_cast<long long>(p.div_bt.div(tok)) * p.n + st;
+      float f = 0.f, lv = 0.f;
+      if (in_bounds(si, 1, p.ext_scale, p.status)) {
+        f = __ldg(p.ks + si) * p.scale_log2;
+        const float vs = __ldg(p.vs + si);
+        lv = vs == 0.f ? static_cast<float>(kQ8MinExp) : log2f(vs);
+      }
+      for (int u0 = 0; u0 < min(32, to - c32); u0 += U) {
+        float s[U], y[U], v[U][4], top = -INFINITY;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const long long at_key = min(c32 + u0 + u, to - 1) * step;
+          float x[4], dot = 0.f;
+          codes(kc + at_key, lane, x);
+          codes(vc + at_key, lane, v[u]);
+#pragma unroll
+          for (int i = 0; i < E; ++i) dot = fmaf(q[i], x[i], dot);
+#pragma unroll
+          for (int d = 16; d > 0; d /= 2) dot += __shfl_xor_sync(0xffffffffu, dot, d);
+          const float fu = __shfl_sync(0xffffffffu, f, u0 + u);
+          // (dot times either factor alone may pass fp32, and the factors' product where dot is 0)
+          s[u] = fabsf(rf * fu) < INFINITY ? dot * (rf * fu) : dot * rf * fu;
+          y[u] = s[u] + __shfl_sync(0xffffffffu, lv, u0 + u);
+          if (c32 + u0 + u >= to) s[u] = y[u] = -INFINITY;
+          top = fmaxf(top, y[u]);
+        }
+        if (top - 13.f > m) {
+          const float d = m - (top - 13.f), alpha = fast_exp2(d);
+          l = add_scaled(0.f, l, d, alpha);
+#pragma unroll
+          for (int i = 0; i < E; ++i) o[i] *= alpha;
+          m = top - 13.f;
+        }
+        const float mu = m == -INFINITY ? 0.f : m;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const float w = fast_exp2(y[u] - mu);
+          // s - m is at most 13 - lv <= 73; with the 2^20 a key that is 2^-36 of the one that set m, of a scale of
+          // 2^121, is still in fp32's range, and 2^28 of those of the smallest scale are within it
+          l += y[u] == y[u] ? fast_exp2(s[u] - mu + 20.f) : y[u];
+#pragma unroll
+          for (int i = 0; i < E; ++i) o[i] = fmaf(w, v[u][i], o[i]);
+        }
+      }
+    }
+    l *= 0x1p-20f;
+    if (at.last() - at.r0 == at.rounds) {
+      const float inv = 1.f / l;
+#pragma unroll
+      for (int i = 0; i < E; ++i) p.o[qrow * D + lane * E + i] = __float2bfloat16_rn(o[i] * inv);
+      if (lane == 0) p.lse[li] = (m + __log2f(l)) * kLn2;
+      return;
+    }
+    const long long pi = part_row(p, hk, row0, b * p.groups + grp + cta, lr);
+    if (!in_bounds(pi, 1, p.ext_part, p.status)) return;
+#pragma unroll
+    for (int i = 0; i < E; ++i) p.part_o[pi * D + lane * E + i] = o[i];
+    if (lane == 0) reinterpret_cast<float2*>(p.part_ml)[pi] = make_float2(m, l);
+  }
+};
+
 template <int D, int FMT, int TR>
 __global__ void __launch_bounds__(kQThreads, Q8Smem<D, TR>::CTAS)
-    decode_q8_split_kernel(const DecodeQ8Params p, const __grid_constant__ CUtensorMap tmK,
+    decode_q8_split_kernel(const __grid_constant__ DecodeQ8Params p, const __grid_constant__ CUtensorMap tmK,
                            const __grid_constant__ CUtensorMap tmV) {
   using SM = Q8Smem<D, TR>;
   constexpr int S = SM::STAGES, ROWS = TR;
@@ -596,6 +774,7 @@ __global__ void __launch_bounds__(kQThreads, Q8Smem<D, TR>::CTAS)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   float* row_fac = reinterpret_cast<float*>(smem + SM::RING + SM::Q + SM::FAC + SM::BARS);  // [ROWS]
   volatile int* abort_flag = reinterpret_cast<volatile int*>(row_fac + ROWS);
+  volatile int* again = abort_flag + 1;  // V scales were too far apart
   const uint32_t bars = sQ + SM::Q + SM::FAC + warp * S * 8;
   const uint32_t ring = sRing + warp * S * 2 * SM::KV;
   if (lane == 0) {
@@ -604,7 +783,7 @@ __global__ void __launch_bounds__(kQThreads, Q8Smem<D, TR>::CTAS)
     tc::fence_async_smem();
   }
   if (tid == 0) {
-    *abort_flag = 0;
+    *abort_flag = *again = 0;
     tc::tma_prefetch_desc(&tmK);
     tc::tma_prefetch_desc(&tmV);
   }
@@ -735,6 +914,7 @@ __global__ void __launch_bounds__(kQThreads, Q8Smem<D, TR>::CTAS)
   const float key_fac = p.scale_log2 * __int_as_float((127 + down) << 23);
   const uint32_t sFac = sQ + SM::Q + warp * (kQTile * 12);
   float* fac = reinterpret_cast<float*>(smem + SM::RING + SM::Q) + warp * (kQTile * 3);
+  float vs_lo = INFINITY, vs_hi = 0.f;  // V scales of this lane's keys
   int done = 0;  // tiles whose copies have arrived
   for (; done < tiles; ++done) {
     const int st = (it + done) % S;
@@ -744,6 +924,10 @@ __global__ void __launch_bounds__(kQThreads, Q8Smem<D, TR>::CTAS)
       const uint32_t vbits = __float_as_uint(vs);
       const int e = static_cast<int>((vbits >> 23) & 0xffu) - 127;
       const bool fin = e < 128 && e > -127;
+      if (fin) {
+        vs_lo = fminf(vs_lo, vs);
+        vs_hi = fmaxf(vs_hi, vs);
+      }
       // A scale that is no number (its block took in one) makes the scores of its
       // visible keys NaN. One of zero (never written) counts as the smallest.
       const float kf = ks * key_fac;
@@ -780,8 +964,24 @@ __global__ void __launch_bounds__(kQThreads, Q8Smem<D, TR>::CTAS)
   float* mbuf = reinterpret_cast<float*>(smem);
   constexpr int RS = D + 4;
   rows.store(mbuf + warp * ROWS * RS, lane);
+  // (columns D + 2 and D + 3 are free; positive floats are ordered as their bits are)
+  const uint32_t lo = __reduce_min_sync(0xffffffffu, __float_as_uint(vs_lo));
+  const uint32_t hi = __reduce_max_sync(0xffffffffu, __float_as_uint(vs_hi));
+  if (lane == 0)
+    *reinterpret_cast<uint2*>(mbuf + warp * ROWS * RS + D + 2) = make_uint2(lo, hi);
   __syncthreads();
   if (*abort_flag) return;
+  if (tid == 0) {
+    float lo4 = INFINITY, hi4 = 0.f;
+#pragma unroll
+    for (int w = 0; w < kQWarps; ++w) {
+      lo4 = fminf(lo4, mbuf[w * ROWS * RS + D + 2]);
+      hi4 = fmaxf(hi4, mbuf[w * ROWS * RS + D + 3]);
+    }
+    // A weight is lost 2^-126 below the reference, 2^-139 of the largest: with scales closer than this its key is
+    // 2^-63 of the largest weight's in l.
+    if (hi4 * 0x1p-76f > lo4) *again = 1;
+  }
   const bool all = r1 - r0 == rounds;
   for (int i = tid; i < valid_rows * (D / 4); i += kQThreads) {
     const int lr = i / (D / 4), col4 = (i % (D / 4)) * 4;
@@ -830,6 +1030,9 @@ __global__ void __launch_bounds__(kQThreads, Q8Smem<D, TR>::CTAS)
   tc::fence_async_smem();  // the merge's writes come before the copies that replace them
   __syncthreads();
   }
+  __syncthreads();
+  if (!*again) return;
+  Q8Again<D, FMT, ROWS>::run(p);
 }
 
 // The parts of a query row joined, one CTA a row: its groups of D / 4 threads
@@ -885,18 +1088,18 @@ __global__ void __launch_bounds__(kQThreads) decode_q8_combine_kernel(const Deco
 #pragma unroll
     for (int u = 0; u < U; ++u) top = fmaxf(top, ml[u].x);
     const float mu = top == -INFINITY ? 0.f : top, f = fast_exp2(m - mu);
-    m = top;
-    l *= f;
     acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const float g = fast_exp2(ml[u].x - mu);
-      l += g * ml[u].y;
+      l = u == 0 ? add_scaled(add_scaled(0.f, ml[0].y, ml[0].x - mu, g), l, m - mu, f)
+                 : add_scaled(l, ml[u].y, ml[u].x - mu, g);
       acc.x += g * v[u].x;
       acc.y += g * v[u].y;
       acc.z += g * v[u].z;
       acc.w += g * v[u].w;
     }
+    m = top;
   }
   if (tid % LPR == 0) ref[tid / LPR] = make_float2(m, l);
   sum[tid / LPR][tid % LPR] = acc;
@@ -912,7 +1115,7 @@ __global__ void __launch_bounds__(kQThreads) decode_q8_combine_kernel(const Deco
   for (int i = 0; i < G; ++i) {
     const float g = fast_exp2(ref[i].x - mu);
     const float4 v = sum[i][tid];
-    l += g * ref[i].y;
+    l = add_scaled(l, ref[i].y, ref[i].x - mu, g);
     acc.x += g * v.x;
     acc.y += g * v.y;
     acc.z += g * v.z;
