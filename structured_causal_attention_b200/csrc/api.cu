@@ -335,8 +335,7 @@ int decode_q8_call(const void* q, const void* k_codes, const void* v_codes, cons
                    int Tcap, int Hq, int Hkv, int D, int format, int block_tokens, int mode,
                    int W_tokens, int final_only, float scale, void* workspace, size_t workspace_bytes,
                    void* stream) {
-  if (!q || !k_codes || !v_codes || !k_scale || !v_scale || !seqlen || !out || !lse || !workspace)
-    return HD_ERR_INVALID_ARG;
+  if (!q || !k_codes || !v_codes || !k_scale || !v_scale || !seqlen || !out || !lse) return HD_ERR_INVALID_ARG;
   const int st = check_q8(B, n, Tcap, Hkv, D, format, block_tokens);
   if (st != HD_OK) return st;
   if (mode < HD_INTRA || mode > HD_CROSS_WINDOW) return HD_ERR_INVALID_ARG;
@@ -347,7 +346,8 @@ int decode_q8_call(const void* q, const void* k_codes, const void* v_codes, cons
     return HD_ERR_INVALID_ARG;
   const int fits = check_decode_q8(B, n, Tcap, Hq, Hkv, D);
   if (fits != HD_OK) return fits;
-  if (workspace_bytes < decode_q8_workspace(B, n, Tcap, Hq, Hkv, D, final_only)) return HD_ERR_INVALID_ARG;
+  // (after the sizes: those that are refused need 0 bytes, and a buffer of 0 bytes may have no address)
+  if (!workspace || workspace_bytes < decode_q8_workspace(B, n, Tcap, Hq, Hkv, D, final_only)) return HD_ERR_INVALID_ARG;
   DecodeQ8Params p = {};
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.kc = static_cast<const uint8_t*>(k_codes);
