@@ -259,6 +259,10 @@ def kv_cache_q8(B, Tcap, n, Hkv, D, dtype, block_tokens=16, device="cuda"):
     """An empty 8-bit cache for ``Tcap`` tokens; ``dtype`` is torch.float8_e4m3fn or torch.int8."""
     import torch
 
+    if min(B, Tcap, n, Hkv, D, block_tokens) < 1:
+        raise ValueError("sizes and block_tokens must be positive")
+    if dtype not in (torch.float8_e4m3fn, torch.int8):
+        raise ValueError("dtype must be float8_e4m3fn or int8")
     k, v = (torch.zeros((B, Tcap * n, Hkv, D), dtype=dtype, device=device) for _ in range(2))
     k_scale, v_scale = (torch.zeros((B, Hkv, -(-Tcap // block_tokens), n), dtype=torch.float32, device=device)
                         for _ in range(2))

@@ -40,3 +40,12 @@ def test_helpers_name_unsupported_sizes(call, rows):
     with pytest.raises(hd.HDError) as e:
         call(q, cache, torch.ones(1, dtype=torch.int32, device="cuda"), hd.CROSS_FULL)
     assert e.value.status == hd.HD_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("kw", [dict(block_tokens=0), dict(block_tokens=-16), dict(n=0), dict(Tcap=0), dict(B=0), dict(Hkv=0),
+                                dict(D=0), dict(dtype=torch.bfloat16), dict(dtype=torch.uint8), dict(dtype=torch.float8_e5m2)])
+def test_a_cache_of_bad_sizes_is_not_made(kw):
+    a = dict(B=1, Tcap=8, n=2, Hkv=2, D=64, dtype=torch.int8, block_tokens=16, device="cpu")
+    hd.kv_cache_q8(**a)
+    with pytest.raises(ValueError):
+        hd.kv_cache_q8(**dict(a, **kw))
