@@ -40,6 +40,7 @@
 #include "hd_common.cuh"
 #include "launch.h"
 #include "tc_ptx.cuh"
+#include "tensor_map.h"
 
 namespace hd {
 
@@ -453,23 +454,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ----------------------------------------------------------------- host side
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  if (!fn) {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(ptr);
-  }
-  return fn;
-}
-
 // (d, j, row, batch) view; strides in elements; box (box_d, 1, box_rows, 1).
 bool make_map(CUtensorMap* map, const void* base, bool fp32, int D, long long J, long long R,
               long long B, long long stride_j, long long stride_r, long long stride_b, int box_d,

@@ -45,6 +45,7 @@
 #include "hd_common.cuh"
 #include "launch.h"
 #include "tc_ptx.cuh"
+#include "tensor_map.h"
 
 namespace hd {
 
@@ -379,23 +380,6 @@ __global__ void __launch_bounds__(kThreads, 2)
 }
 
 // ----------------------------------------------------------------- host side
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  if (!fn) {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(ptr);
-  }
-  return fn;
-}
-
 // bf16 tensor viewed as (d, j, row, batch) with a box of 64 x 1 x 128 x 1.
 bool make_map(CUtensorMap* map, const void* base, int D, long long J, long long R, long long B,
               long long stride_j, long long stride_r, long long stride_b) {

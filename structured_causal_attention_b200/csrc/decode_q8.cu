@@ -58,6 +58,7 @@
 #include "hd_common.cuh"
 #include "launch.h"
 #include "tc_ptx.cuh"
+#include "tensor_map.h"
 
 namespace hd {
 
@@ -1125,23 +1126,6 @@ __global__ void __launch_bounds__(kQThreads) decode_q8_combine_kernel(const Deco
   *reinterpret_cast<uint2*>(p.o + orow * D + tid * 4) =
       make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
   if (tid == 0) p.lse[li] = (top + __log2f(l)) * kLn2;
-}
-
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  if (!fn) {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(ptr);
-  }
-  return fn;
 }
 
 // The codes as (d, head or (stream, head), row, sequence), a box of one tile.

@@ -32,6 +32,7 @@
 #include "hd_common.cuh"
 #include "launch.h"
 #include "tc_ptx.cuh"
+#include "tensor_map.h"
 
 namespace hd {
 
@@ -482,19 +483,8 @@ __global__ void __launch_bounds__(256) final_readout_kernel(const uint8_t* __res
 // box of 64 x box_rows, 128-byte swizzle.
 bool make_map_2d(CUtensorMap* map, const void* base, long long d, long long rows,
                  long long row_stride, int box_rows) {
-  using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                     const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                     const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                     CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-  static EncodeTiledFn fn = nullptr;
-  if (!fn) {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      return false;
-    fn = reinterpret_cast<EncodeTiledFn>(ptr);
-  }
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(rows)};
   const cuuint64_t strides[1] = {static_cast<cuuint64_t>(row_stride * 2)};
   const cuuint32_t box[2] = {static_cast<cuuint32_t>(kLK), static_cast<cuuint32_t>(box_rows)};
