@@ -158,13 +158,6 @@ __device__ __forceinline__ float2 f32x2_parts(uint64_t a) {
   asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(a));
   return f;
 }
-// A load that stays where it is written: the compiler moved a plain one down to
-// its use in the next step, whose wait for it took a fifth of the time.
-__device__ __forceinline__ float ldg_here(const float* at) {
-  float x;
-  asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(x) : "l"(at));
-  return x;
-}
 __device__ __forceinline__ float lds32(uint32_t addr) {
   float r;
   asm volatile("ld.shared.f32 %0, [%1];" : "=f"(r) : "r"(addr));
@@ -856,8 +849,8 @@ __global__ void __launch_bounds__(kQThreads, Q8Smem<D, TR>::CTAS)
     vs = 1.f;
     const long long si = sc0 + static_cast<long long>(blk) * p.n + stream;
     if (key < ce && in_bounds(si, 1, p.ext_scale, p.status)) {
-      ks = ldg_here(p.ks + si);
-      vs = ldg_here(p.vs + si);
+      ks = __ldg(p.ks + si);
+      vs = __ldg(p.vs + si);
     }
     key += kQWarps * kQTile;
     blk += p.step_blk;
