@@ -339,8 +339,11 @@ int hd_decode_attn_noalloc(const void* q, const void* k_cache, const void* v_cac
  *                up to 8 significant bits
  *   No scale is smaller than 2^-60.
  * Supported: D in {64, 128}, 1 <= block_tokens <= 1024 (16 to 64 are usual).
- * Codes and scales are those hd_kv_write_q8 writes; a cache need not be
- * initialised, but a token is read only after it was written.
+ * Codes and scales are those hd_kv_write_q8 writes, in buffers that start on
+ * 16-byte boundaries. A token is read only after it was written. Codes need not be
+ * initialised; scales need not where each block's first token is written before
+ * its others or with them, and have to be 0 elsewhere, as a write that enters a
+ * block behind its first token goes by the scale that it finds.
  */
 typedef enum { HD_Q8_E4M3 = 0, HD_Q8_INT8 = 1 } hd_q8_format;
 
@@ -357,9 +360,11 @@ typedef enum { HD_Q8_E4M3 = 0, HD_Q8_INT8 = 1 } hd_q8_format;
  * A block whose first token is written starts afresh, whatever it held. A block
  * that was begun before keeps its scale or, where the new rows need a larger
  * one, is raised to that, and the codes of its earlier tokens are rounded
- * again, code * old / new. Codes of other tokens stay as they are. (A block
- * that is entered behind its first token, with that never written, has to hold
- * a scale of 0.)
+ * again, code * old / new. Codes of other tokens stay as they are: those behind
+ * the written ones in their last block no longer count, as its scale may be
+ * another, and are written again with a token that is replaced before them. (A
+ * block that is entered behind its first token, with that never written, has to
+ * hold a scale of 0.)
  * If a written row holds a NaN or an infinity, its block's scale of that stream
  * and head becomes NaN (and stays so until the block starts afresh): every
  * value of it reads as NaN, and so does each attention output that sees one.
@@ -397,7 +402,10 @@ size_t hd_decode_final_q8_workspace_bytes(int B, int n, int Tcap, int Hq, int Hk
  * q, seqlen, out, lse, mode, W_tokens, scale, the precondition (the new token's
  * n rows are in the cache) and the errors are theirs; the cache is as above.
  * Scores and softmax are fp32 and the scales are applied in fp32; the weights
- * are rounded to fp16 before they meet the V codes. Supported: as there, with
+ * are rounded to fp16 before they meet the V codes. A call with the same inputs
+ * gives the same bits; how a sequence's keys are divided among the GPU, and so the
+ * order of its sums and its last bits, goes by the lengths of the whole batch.
+ * Supported: as there, with
  * B*n*Hq*ceil(Tcap*n / 128) <= 2^30 and Tcap*n*Hkv*D < 2^40.
  */
 int hd_decode_attn_q8(const void* q, const void* k_codes, const void* v_codes, const float* k_scale,

@@ -244,8 +244,9 @@ def lm_head_ce_bwd(x, w, labels, lse, n, grad_scale=1.0, stream=None, workspace=
 
 class KVCacheQ8(NamedTuple):
     """An 8-bit KV cache: codes [B, Tcap*n, Hkv, D], float8_e4m3fn or int8 (the format), and fp32 scales
-    [B, Hkv, ceil(Tcap / block_tokens), n]. ``kv_cache_q8`` makes one; any four tensors of these
-    shapes do, as what they hold is written by ``kv_write_q8``."""
+    [B, Hkv, ceil(Tcap / block_tokens), n]. ``kv_cache_q8`` makes one. Other contiguous tensors of these shapes do
+    where their storage starts on 16-byte boundaries, with scales of 0 (any, where each block is written from its
+    first token on): a write that enters a block behind its first token goes by the scale that it finds."""
 
     k: Any
     v: Any
@@ -327,7 +328,9 @@ def _index_q8(t, B, what):
 
 def kv_write_q8(k, v, cache, token_offset=None, lengths=None, stream=None):
     """Quantise k, v bf16 [B, L*n, Hkv, D] into ``cache`` (a KVCacheQ8) from token ``token_offset[b]`` on
-    (int32 [B]; None: 0). ``lengths`` (int32 [B]) gives the tokens of each sequence in a padded batch."""
+    (int32 [B]; None: 0). ``lengths`` (int32 [B]) gives the tokens of each sequence in a padded batch. What the last
+    written block holds behind the written tokens no longer counts: to replace a token, write those behind it in its
+    block again too."""
     import torch
 
     _need_cuda(k, v)
