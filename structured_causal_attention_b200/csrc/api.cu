@@ -28,7 +28,7 @@ int* status_ptr() {
 bool aligned16(const void* ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 15u) == 0; }
 
 constexpr long long kMaxPositions = 1LL << 28;  // positions and rows stay far below kWinInf
-constexpr int kMaxBlockTokens = 1024;  // one warp quantises a block of a stream and head
+constexpr int kMaxBlockTokens = 1024;  // up to eight warps of a CTA quantise a block of a stream and head
 
 int q8_blocks(int tokens, int block_tokens) {
   return static_cast<int>((static_cast<long long>(tokens) + block_tokens - 1) / block_tokens);

@@ -15,11 +15,11 @@
 // with a query of two 8-bit terms, are 2-5% faster, but an error of 2^-16 of a
 // row's largest element is too much for its lse.) A query row is multiplied by the
 // power of two that puts its largest magnitude in [2^14, 2^15): exact but for
-// elements 2^29 and more below it, which keep an error of 2^-40 of it.
+// elements 2^29 and more below it, which keep an error of 2^-39 of it.
 //
 // With s in log2 units the weight of a key is w_j = vs_j 2^(s_j - M). M follows the
 // running maximum of s + log2 vs: it is set so that the largest weight is 2^13,
-// and again once one passes 2^15, so that weights fit fp16 (rounding 2^-12, kept
+// and again once one passes 2^15, so that weights fit fp16 (rounding 2^-11, kept
 // down to 2^-27 of the largest). The softmax's sum takes the same weights without
 // the scale, l += w_j / vs_j, in fp32. So blocks of very different size need no
 // common scale, and O / l needs no correction. A weight below fp32's range counts
@@ -32,8 +32,10 @@
 // tile of 8 is the N of the MMAs (half the MMAs and exponentials of 16 rows that
 // are half padding: 200 -> 190 us, and with two CTAs an SM 176), 16 are their M,
 // and of 32 the codes are converted once for two such M (B8, 8192 tokens, 32 rows:
-// 194 -> 141 us). One mma.sync tile of rows is all that the keys meet, so tcgen05's
-// M of 64 and more would be padding, and its operands 8-bit terms (see above).
+// 194 -> 141 us). The keys meet few rows, so as tcgen05's M of 64 and more the rows
+// would be padding. With keys as M the codes of K could be its operand as they lie,
+// with the query as three 8-bit terms; that was not built. P cannot be such terms: the
+// many small weights of a long cache add up to more than their floor.
 //
 // The work is one line of rounds of 128 keys for each KV head: all rounds of the
 // first problem (sequence, stream group), then of the next, as the lengths on the
@@ -48,10 +50,11 @@
 // problem that one CTA has whole is written by it; of the others each part goes
 // to the workspace, and a second kernel joins them.
 //
-// HBM bounds it, at the power cap's clock with the conversions close behind:
-// B8, 16385 tokens, 32/8 heads of 128, 1.08 GB: 192 us E4M3 (5.6 TB/s), its
-// final-stream step 176 us (6.1 TB/s); B64 INT8, 8.6 GB, 1.58 ms (5.4 TB/s; 1.37 ms,
-// 6.3 TB/s, before the clock falls).
+// HBM bounds it, at the power cap's clock with the conversions close behind. Held
+// for seconds (in short bursts), 16385 tokens, 32/8 heads of 128: B8, 1.08 GB, 193 us
+// E4M3 (196) and 213 INT8 (184), its final-stream step 168 (164) and 183 (165), INTRA
+// 178 and 186; B64, 8.6 GB, 1.49 ms E4M3 and 1.66 INT8 (5.2 TB/s; 1.39 ms, 6.2 TB/s, before
+// the clock falls), INTRA 1.46 and 1.45.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -73,9 +76,11 @@ constexpr float kLn2 = 0.69314718055994530942f;
 // CTAs of an SM. The copies that three keep in flight are more than HBM serves
 // best, but a tile of 16 rows has so much to compute that three are faster all the
 // same: 64 sequences of 16385 tokens in INT8 took 1574 us with three and 1650 with
-// two, 8 in E4M3 191 and 196. With 8 rows two are: 8 sequences' final streams 190
-// and 176. At D = 64, with tiles of half the bytes, three are (102 and 111 us).
-// Two row tiles need the registers of two.
+// two, 8 in E4M3 191 and 196. With 8 rows two are: three and two took 188 and 164 us for
+// 8 sequences' final streams in E4M3, 191 and 178 for their INTRA step (INT8 194 and
+// 176), 1606 and 1398 for that of 64 in INT8, 374 and 347 for 64 final INTRA streams; only with
+// one KV head are three faster (INTRA, 16 sequences: 78 and 82). At D = 64, with tiles
+// of half the bytes, three are (102 and 111 us). Two row tiles need the registers of two.
 constexpr int q8_ctas_per_sm(int D, int tile_rows) { return tile_rows == 32 || (tile_rows == 8 && D == 128) ? 2 : 3; }
 
 // TR query rows a CTA: 8, 16 or 32 (two tiles of 16, the codes converted once for
@@ -1122,7 +1127,10 @@ __global__ void __launch_bounds__(kQThreads) decode_q8_combine_kernel(const Deco
 }
 
 // The codes as (d, head or (stream, head), row, sequence), a box of one tile.
-// Promotion to 256 bytes brings the next head's row of a key along: 206 -> 195 us.
+// Promotion to 256 bytes brings the next head's row of a key along: against 128 bytes
+// 205 -> 196 us (B8, E4M3, CROSS_FULL), 185 -> 177 under INTRA. Where a row under INTRA has
+// fewer than 256 bytes it brings another stream's, used later or not at all: 16 sequences with one
+// KV head of 128 take 82 us with it and 68 with 128 bytes, of 64 55 and 51, with two of 64 80 and 74.
 template <int D>
 bool make_map(CUtensorMap* map, const uint8_t* base, long long J, long long R, long long B) {
   EncodeTiledFn fn = encode_fn();
@@ -1180,8 +1188,10 @@ int decode_q8_tile_rows(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
 // CTAs of a line (of `lines` KV heads and row tiles), the rounds that a piece has at
 // least, and whether each CTA takes one problem whole instead of a piece: where
 // none has more than kWhole rounds, dividing one and joining its parts takes
-// longer than it saves (B8, 8 rounds: 14.3 us and 13.0; 16 rounds: 15.4 and 21), and
-// the second kernel is left out.
+// longer than it saves, and the second kernel is left out. It goes by the rounds alone, a
+// compromise: in pieces and whole, of 8 rounds, 64 problems and heads (B8 CROSS_FULL) take
+// 20.5 and 18.4 us, 256 (INTRA) 26.6 and 22.6, 2048 107 and 89, but 8 16.1 and 18.4; of 16
+// rounds 64 26.6 and 26.6, 256 38.9 and 34.8, 2048 185 and 163, but 8 16.4 and 26.6.
 void decode_q8_plan(long long problems, long long most_keys, int D, int tile_rows, long long lines, int sms, int* ctas,
                     int* least, int* whole) {
   constexpr int kWhole = 8;

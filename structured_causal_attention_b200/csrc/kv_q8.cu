@@ -23,7 +23,8 @@
 // block, stream, head): they alone read and write that scale and those codes, so
 // no atomics and no order between units. They hold the block's rows in registers
 // between finding their largest magnitude and storing their codes, so each row is
-// read once. Rows of neighbouring heads are neighbours in memory and so are their
+// read once; of a block longer than the 128 (D = 128) or 256 that eight warps hold, the
+// rows past those are read twice. Rows of neighbouring heads are neighbours in memory and so are their
 // warps. Reading: eight codes a thread, four such in flight.
 //
 // HBM bounds both: 4 x 16385 tokens, 4 streams, 8 heads of 128 (3 bytes an element
