@@ -848,10 +848,9 @@ __global__ void __launch_bounds__(kQThreads, Q8Smem<D, TR>::CTAS)
   int tok = intra ? key : static_cast<int>(p.div_n.div(key));
   int stream = intra ? p.s0 + grp : key - tok * p.n;
   int blk = static_cast<int>(p.div_bt.div(tok)), off = tok - blk * p.bt;
-  float ks = 0.f, vs = 1.f;
+  float ks, vs;
   auto fetch_scales = [&]() {
-    ks = 0.f;
-    vs = 1.f;
+    ks = vs = 0.f;  // behind the piece: as never written, and hidden
     const long long si = sc0 + static_cast<long long>(blk) * p.n + stream;
     if (key < ce && in_bounds(si, 1, p.ext_scale, p.status)) {
       ks = __ldg(p.ks + si);
